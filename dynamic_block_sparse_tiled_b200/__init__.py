@@ -30,12 +30,13 @@ __all__ = [
     "blasst_decode_mla_workspace_bytes", "attention_decode_mla",
     "attention_prefill", "attention_backward", "attention_decode", "new_stats", "stats_dict",
     "BLASST_OK", "BLASST_EINVAL", "BLASST_EUNSUPPORTED", "BLASST_ECUDA", "BLASST_ETIMEOUT",
-    "BLASST_EWORKSPACE", "BLASST_BF16", "BLASST_FP32",
+    "BLASST_EWORKSPACE", "BLASST_EINDEX", "BLASST_BF16", "BLASST_FP32", "BLASST_FP16",
 ]
 
 BLASST_OK, BLASST_EINVAL, BLASST_EUNSUPPORTED, BLASST_ECUDA, BLASST_ETIMEOUT, BLASST_EWORKSPACE = (
     0, -1, -2, -3, -4, -5)
-BLASST_BF16, BLASST_FP32 = 0, 1
+BLASST_EINDEX = -6
+BLASST_BF16, BLASST_FP32, BLASST_FP16 = 0, 1, 2
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libblasst.so")
@@ -450,3 +451,10 @@ def attention_decode(q, k_cache, v_cache, *, lam=0.0, Bc=128, num_splits=64, wit
     blasst_decode(q, k_cache, v_cache, o, lse, lam=lam, Bc=Bc, num_splits=num_splits,
                   workspace=workspace, skip_mask_out=mask, stats_out=stats, stream=stream)
     return o, lse, mask
+
+
+# operators over sequences of different lengths (they use the names above)
+from .sequences import *  # noqa: E402,F401,F403
+from .sequences import __all__ as _sequence_names  # noqa: E402
+
+__all__ += _sequence_names

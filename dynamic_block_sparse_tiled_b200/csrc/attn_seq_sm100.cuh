@@ -1,0 +1,916 @@
+// attn_seq_sm100.cuh - exact attention over sequences of different lengths on
+// sm_100a (tcgen05 + TMEM + TMA): prompts packed one behind the other, or new
+// tokens (a chunk or a single one per sequence) against a paged KV cache.
+//
+// o_i = sum_j p_ij v_j / sum_j p_ij, p_ij = exp(scale q_i . k_j - m_i) over
+// the keys j the mask leaves, one pass over the keys with a running reference
+// m and sum l per row; lse_i = m + ln l. A row without keys gets o = 0,
+// lse = -inf.
+//
+// A tile is 128 rows, each one (token, query head of one KV head's group):
+// g = Hq / Hkv heads of floor(128 / g) tokens. All heads of a group share
+// every K and V tile, and the causal diagonal crosses 128 / g tokens only. A
+// CTA runs two streams of (S = Q K^T, softmax, O += P V), one softmax
+// warpgroup each, so that the tensor core works on one stream while the other
+// takes its exponentials:
+//   two tiles  (more than 128 rows left): stream s owns rows tile s; both read
+//              each K and V block once it is in shared memory;
+//   one tile   (up to 128 rows, e.g. single tokens): both streams own the same
+//              rows and take the even and the odd key blocks; their sums are
+//              joined from TMEM at the end.
+// Warps 0-3, 4-7: softmax of stream 0, 1 (thread = row = TMEM lane); warp 8:
+// TMA producer; warp 9: tcgen05 issuer; warp 10: finds the CTA's items and
+// hands the others one record each (11 only fills the warpgroup, which gives
+// registers to the softmax warps). TMEM: S0, S1 (fp32, 128 columns; P as
+// 16-bit pairs over the first 64 of the same columns once S is in registers),
+// O0, O1.
+//
+// Work: either one item (sequence, KV head, tile) per CTA, the last tiles of
+// a head first (enough tiles to fill the GPU several times), or a resident
+// grid that cuts the list of all key blocks of all items into equal ranges
+// ("shared list"): an item cut by a range's end leaves fp32 partials, joined
+// by seq_join_kernel in the order of the ranges, so results do not depend on
+// timing.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/blasst.h"
+#include "ptx_sm100.cuh"
+
+namespace blasst {
+
+struct SeqAttnParams {
+  void* o;     // [Tq, Hq, D]
+  float* lse;  // [Tq, Hq]
+  const int* cu_q;
+  const int* cu_k;     // packed keys; null with a page table
+  const int* kv_lens;  // with a page table
+  const int* table;
+  long long table_stride;
+  int table_width;
+  int page_size, n_pages;
+  int chunk;  // keys per TMA box: 128, or the largest power of two that divides page_size
+  int n_seq, Tq, Tk, Hq, Hkv, g;
+  int rt;        // tokens per 128-row tile
+  int n_tiles;   // most tiles per KV head (one item per CTA); 0: shared list
+  int causal;
+  float scale_log2;
+  float* part_o;    // [2 * grid][256][D]
+  float* part_lse;  // [2 * grid][256], log2 units
+  int4* part_desc;  // [grid][2]
+  int* err;
+  uint64_t timeout_ns;
+};
+
+// One sequence's place in q and in the keys, read from the device arrays and
+// clamped to the tensors (a clamp is reported: BLASST_EINDEX).
+struct SeqSpan {
+  int q0, qlen, k0, kvlen, off, tiles;
+};
+
+__device__ __forceinline__ void seq_record_error(int* err, int code) {
+  if (err) atomicCAS(err, 0, code);
+}
+
+__device__ __forceinline__ SeqSpan seq_span(const int* cu_q, const int* cu_k, const int* kv_lens,
+                                            int kv_cap, int Tq, int Tk, int tile_tokens, int s,
+                                            int* err) {
+  SeqSpan r;
+  const int q0 = cu_q[s], q1 = cu_q[s + 1];
+  r.q0 = min(max(q0, 0), Tq);
+  r.qlen = min(max(q1, r.q0), Tq) - r.q0;
+  bool bad = q0 < 0 || q1 < q0 || q1 > Tq;
+  if (cu_k) {
+    const int a = cu_k[s], b = cu_k[s + 1];
+    r.k0 = min(max(a, 0), Tk);
+    r.kvlen = min(max(b, r.k0), Tk) - r.k0;
+    bad = bad || a < 0 || b < a || b > Tk;
+  } else {
+    const int n = kv_lens[s];
+    r.k0 = 0;
+    r.kvlen = min(max(n, 0), kv_cap);
+    bad = bad || n != r.kvlen;
+  }
+  if (bad) seq_record_error(err, BLASST_EINDEX);
+  r.off = r.kvlen - r.qlen;
+  r.tiles = (r.qlen + tile_tokens - 1) / tile_tokens;
+  return r;
+}
+
+template <int D>
+struct SeqAttnCfg {
+  static constexpr int NTHREADS = 384;
+  // registers per thread: a softmax thread keeps its 128 scores; 2 x 216 + 72
+  // = 3 x 168, what the launch has
+  static constexpr int REGS = 168, REGS_SOFT = 216, REGS_REST = 72;
+  static constexpr int NSOFT = 256;
+  static constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_ITEM = 10;
+  static constexpr int BK = 128;
+  static constexpr int DBOX = D / 64;
+  static constexpr int BOX = 128 * 128;  // [128 rows][64 columns], 16 bits
+  static constexpr int TILE = BOX * DBOX;
+  static constexpr int NST = D == 128 ? 5 : 8;  // K / V ring
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_KV = 2 * TILE;
+  static constexpr int OFF_BAR = OFF_KV + NST * TILE;
+  static constexpr int B_Q = 0;
+  static constexpr int B_TAIL = 1;          // V rows of a last block landed (then cleared behind the end)
+  static constexpr int B_KVF = 2;           // [NST]
+  static constexpr int B_KVE = B_KVF + NST; // [NST]
+  static constexpr int B_S = B_KVE + NST;   // [2] S written
+  static constexpr int B_P = B_S + 2;       // [2] P written, O rescaled (4 warps)
+  static constexpr int B_DONE = B_P + 2;    // every product of the item done
+  static constexpr int B_OFREE = B_DONE + 1;  // O read (8 warps)
+  static constexpr int B_ML = B_OFREE + 1;  // (m, l) of both streams of a one-tile item (8 warps)
+  static constexpr int B_DRAIN = B_ML + 1;
+  static constexpr int NITEM = 2;
+  static constexpr int B_IF = B_DRAIN + 1;   // [NITEM] item record written
+  static constexpr int B_IE = B_IF + NITEM;  // [NITEM] read (loader, issuer, 8 softmax warps)
+  static constexpr int NBAR = B_IE + NITEM;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  // misc words: [0] tmem base, [1] abort, [3] always 0
+  static constexpr int MISC_BYTES = 16;
+  static constexpr int OFF_ITEM = OFF_MISC + MISC_BYTES;
+  static constexpr int OFF_ML = (OFF_ITEM + NITEM * 48 + 15) / 16 * 16;  // float2 [2][128]
+  static constexpr int SMEM_BYTES = OFF_ML + 2 * 128 * 8;
+  static constexpr int S_COL = 0;    // stream s at 128 s
+  static constexpr int O_COL = 256;  // stream s at 256 + D s
+  static constexpr int TMEM_COLS = 512;
+  static constexpr float TAU = 8.0f;  // the reference moves only by more than 2^8: P <= 256 fits both types
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+};
+
+// shared list: the cost of an item in units of one stream's key block, with a
+// constant for its start and end
+constexpr int kSeqItemCost = 4;
+constexpr int kSeqMinRange = 10;  // every range inside an item then holds a block's start
+
+__device__ __forceinline__ int seq_blocks(const SeqSpan& q, int causal, int tok) {
+  const int keys = causal ? min(max(q.off + tok + 1, 0), q.kvlen) : q.kvlen;
+  return (keys + 127) >> 7;
+}
+
+struct SeqItem {
+  int tok0, ntok, nblk, nblk0, unit;
+  bool one;  // one tile: both streams share its rows
+};
+
+__device__ __forceinline__ SeqItem seq_item(const SeqSpan& q, int causal, int rt, int t) {
+  SeqItem it;
+  it.tok0 = t * 2 * rt;
+  it.ntok = min(2 * rt, q.qlen - it.tok0);
+  it.one = it.ntok <= rt;
+  it.nblk = seq_blocks(q, causal, it.tok0 + it.ntok - 1);
+  it.nblk0 = it.one ? it.nblk : seq_blocks(q, causal, it.tok0 + rt - 1);
+  it.unit = it.one ? 1 : 2;
+  return it;
+}
+
+__device__ __forceinline__ long long seq_cost(const SeqSpan& q, int causal, int rt) {
+  long long c = 0;
+  for (int t = 0; t < q.tiles; ++t) {
+    const SeqItem it = seq_item(q, causal, rt, t);
+    c += kSeqItemCost + static_cast<long long>(it.nblk) * it.unit;
+  }
+  return c;
+}
+
+// Blocks [b0, b1) of an item that starts at `at` in the list and fall into
+// the range [lo, hi): block 0 begins at `at`, block b > 0 behind the constant.
+__device__ __forceinline__ int seq_first_block(long long at, const SeqItem& it, long long lo) {
+  if (lo <= at) return 0;
+  const long long x = lo - at - kSeqItemCost;
+  const long long b = x <= 0 ? 1 : (x + it.unit - 1) / it.unit;
+  return static_cast<int>(b < 1 ? 1 : (b > it.nblk ? it.nblk : b));
+}
+
+// What the roles need to know of an item; vis + token of the tile: keys a row
+// sees (causal), or the sequence's length. seq < 0 ends.
+struct SeqRecord {
+  static constexpr int kWords = 12;
+  static constexpr int kOne = 1, kWhole = 2, kBegins = 4;
+  int hk, qtok, ntok, b0, nb, cnt0, kvlen, k0, vis, seq, mode;
+  __device__ __forceinline__ bool one() const { return mode & kOne; }
+  __device__ __forceinline__ int cnt(int st) const {
+    return st == 0 ? cnt0 : (one() ? nb >> 1 : nb);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t seq_pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t seq_pack2<__nv_bfloat16>(float lo, float hi) {
+  return ptx::pack_bf16x2(lo, hi);
+}
+template <>
+__device__ __forceinline__ uint32_t seq_pack2<__half>(float lo, float hi) {
+  return ptx::pack_f16x2(lo, hi);
+}
+template <typename T>
+struct SeqType;
+template <>
+struct SeqType<__nv_bfloat16> {
+  static constexpr uint32_t kFormat = 1;
+};
+template <>
+struct SeqType<__half> {
+  static constexpr uint32_t kFormat = 0;
+};
+
+template <int D, typename T>
+__global__ void __launch_bounds__(384, 1)
+    blasst_seq_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
+                           const __grid_constant__ CUtensorMap tmK,
+                           const __grid_constant__ CUtensorMap tmV, const SeqAttnParams p) {
+  using C = SeqAttnCfg<D>;
+  constexpr uint32_t IDESC_S = ptx::idesc_f32acc(SeqType<T>::kFormat, 128, 128, false);
+  constexpr uint32_t IDESC_PV = ptx::idesc_f32acc(SeqType<T>::kFormat, 128, D, true);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw;
+  const uint32_t sb = ptx::smem_u32(smem);
+  volatile int* misc = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = misc + 1;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
+  if ((sb & 1023u) != 0u) {  // uniform; the tiles need 1 KB alignment
+    if (threadIdx.x == 0) seq_record_error(p.err, BLASST_EUNSUPPORTED);
+    return;
+  }
+
+  volatile int* items = reinterpret_cast<volatile int*>(smem + C::OFF_ITEM);
+
+  // ---- set-up --------------------------------------------------------------
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NITEM; ++i) {
+      ptx::mbar_init(bar(C::B_IF + i), 1);
+      ptx::mbar_init(bar(C::B_IE + i), 10);
+    }
+    ptx::mbar_init(bar(C::B_Q), 1);
+    ptx::mbar_init(bar(C::B_TAIL), 1);
+    for (int i = 0; i < C::NST; ++i) {
+      ptx::mbar_init(bar(C::B_KVF + i), 1);
+      ptx::mbar_init(bar(C::B_KVE + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar(C::B_S + i), 1);
+      ptx::mbar_init(bar(C::B_P + i), 4);
+    }
+    ptx::mbar_init(bar(C::B_DONE), 1);
+    ptx::mbar_init(bar(C::B_OFREE), 8);
+    ptx::mbar_init(bar(C::B_ML), 8);
+    ptx::mbar_init(bar(C::B_DRAIN), 1);
+    for (int i = 1; i < 4; ++i) misc[i] = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == C::WARP_MMA) {
+    ptx::tmem_alloc(ptx::smem_u32(const_cast<int*>(misc)), C::TMEM_COLS);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+
+  // Item n of the CTA as a role reads it: all lanes get the record, the role
+  // hands the slot back at once (`releases`: one arrival of this warp).
+  auto next_item = [&](int n, SeqRecord& r) -> bool {
+    const int slot = n % C::NITEM;
+    if (!ptx::mbar_wait(bar(C::B_IF + slot), (n / C::NITEM) & 1, abort_flag, p.timeout_ns))
+      return false;
+    const volatile int* w = items + slot * SeqRecord::kWords;
+    r.hk = w[0];
+    r.qtok = w[1];
+    r.ntok = w[2];
+    r.b0 = w[3];
+    r.nb = w[4];
+    r.cnt0 = w[5];
+    r.kvlen = w[6];
+    r.k0 = w[7];
+    r.vis = w[8];
+    r.seq = w[9];
+    r.mode = w[10];
+    return true;
+  };
+  auto item_read = [&](int n) { ptx::mbar_arrive(bar(C::B_IE + n % C::NITEM)); };
+  auto fail = [&]() {
+    *abort_flag = 1;
+    seq_record_error(p.err, BLASST_ETIMEOUT);
+  };
+
+  if (warp >= 8) {
+   ptx::reg_give<C::REGS_REST>();
+   if (warp == C::WARP_ITEM) {
+    // ======================= the CTA's items ================================
+    const int kv_cap = static_cast<int>(
+        min(static_cast<long long>(p.table_width) * p.page_size, 0x7fffff00ll));
+    auto span = [&](int s) -> SeqSpan {
+      return seq_span(p.cu_q, p.cu_k, p.kv_lens, kv_cap, p.Tq, p.Tk, 2 * p.rt, s, p.err);
+    };
+    int n = 0;
+    auto put = [&](int s, const SeqSpan& q, int h, const SeqItem& it, int b0, int b1) -> bool {
+      const int slot = n % C::NITEM;
+      bool ok = true;
+      if (n >= C::NITEM)
+        ok = ptx::mbar_wait(bar(C::B_IE + slot), ((n / C::NITEM) - 1) & 1, abort_flag, p.timeout_ns);
+      ok = __all_sync(0xffffffffu, ok) != 0;
+      if (!ok) return false;
+      if (lane == 0) {
+        volatile int* w = items + slot * SeqRecord::kWords;
+        const bool whole = b0 == 0 && b1 == it.nblk;
+        w[0] = h;
+        w[1] = q.q0 + it.tok0;
+        w[2] = s < 0 ? 0 : it.ntok;
+        w[3] = b0;
+        w[4] = b1 - b0;
+        w[5] = it.one ? (b1 - b0 + 1) >> 1 : max(min(b1, it.nblk0) - b0, 0);
+        w[6] = q.kvlen;
+        w[7] = q.k0;
+        w[8] = p.causal ? q.off + it.tok0 + 1 : q.kvlen;
+        w[9] = s;
+        w[10] = (it.one ? SeqRecord::kOne : 0) | (whole ? SeqRecord::kWhole : 0) |
+                (b0 == 0 ? SeqRecord::kBegins : 0);
+        ptx::mbar_arrive(bar(C::B_IF + slot));
+      }
+      ++n;
+      return true;
+    };
+    // after a wait gave up, calls before blasst_check do nothing
+    const bool live = !(p.err && *reinterpret_cast<volatile int*>(p.err) == BLASST_ETIMEOUT);
+    bool ok = true;
+    if (p.n_tiles != 0) {
+      // ---- one item, counted from the last tile of the last sequence -------
+      const int h = static_cast<int>(blockIdx.x) / p.n_tiles;
+      const int want = static_cast<int>(blockIdx.x) % p.n_tiles;
+      int before = 0;
+      bool found = false;
+      for (int s0 = p.n_seq - 1; s0 >= 0 && !found && live; s0 -= 32) {
+        const int s = s0 - lane;
+        const int tiles = s >= 0 ? span(s).tiles : 0;
+        int upto = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += v;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, want < before + upto);
+        if (hit) {
+          const int l = __ffs(hit) - 1;
+          const int end = before + __shfl_sync(0xffffffffu, upto, l);
+          const SeqSpan q = span(s0 - l);
+          const SeqItem it = seq_item(q, p.causal, p.rt, end - 1 - want);
+          ok = put(s0 - l, q, h, it, 0, it.nblk);
+          found = true;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+      }
+    } else {
+      // ---- this CTA's range of the shared list -----------------------------
+      // no item cut at the range's end, until one is found
+      if (lane == 0) p.part_desc[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+      long long total = 0;
+      for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
+        const int s = s0 + lane;
+        long long c = s < p.n_seq ? seq_cost(span(s), p.causal, p.rt) : 0;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
+        total += c;
+      }
+      total *= p.Hkv;
+      const long long share = (total + gridDim.x - 1) / gridDim.x;
+      const long long range = share < kSeqMinRange ? kSeqMinRange : share;
+      const long long lo = range * blockIdx.x;
+      const long long hi = lo + range < total ? lo + range : total;
+      long long at = 0;  // the list's place of what is looked at
+      int s = 0, h = 0, t = 0;
+      bool found = false;
+      for (int s0 = 0; s0 < p.n_seq && !found && live && lo < total; s0 += 32) {
+        const int sl = s0 + lane;
+        const long long own = sl < p.n_seq ? seq_cost(span(sl), p.causal, p.rt) * p.Hkv : 0;
+        long long upto = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += v;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, lo < at + upto);
+        if (hit) {
+          const int l = __ffs(hit) - 1;
+          at += __shfl_sync(0xffffffffu, upto - own, l);
+          const long long per_head = __shfl_sync(0xffffffffu, own, l) / p.Hkv;
+          s = s0 + l;
+          h = static_cast<int>((lo - at) / per_head);
+          at += h * per_head;
+          found = true;
+        } else {
+          at += __shfl_sync(0xffffffffu, upto, 31);
+        }
+      }
+      if (found) {
+        SeqSpan q = span(s);
+        while (at < hi && ok) {
+          const SeqItem it = seq_item(q, p.causal, p.rt, t);
+          const long long end = at + kSeqItemCost + static_cast<long long>(it.nblk) * it.unit;
+          if (end > lo) {
+            const int b0 = it.nblk ? seq_first_block(at, it, lo) : 0;
+            const int b1 = it.nblk ? seq_first_block(at, it, hi) : 0;
+            // (an item that begins before the range and has no block that
+            // starts in it is the range before's)
+            if (at >= lo || b0 < b1) {
+              if (lane == 0 && b0 == 0 && b1 < it.nblk) {
+                // it goes on in the ranges behind this one: what the join needs
+                p.part_desc[2 * blockIdx.x] =
+                    make_int4(q.q0 + it.tok0, it.ntok, h, it.one ? 1 : 0);
+                p.part_desc[2 * blockIdx.x + 1] =
+                    make_int4(static_cast<int>((end - it.unit) / range), 0, 0, 0);
+              }
+              ok = put(s, q, h, it, b0, b1);
+            }
+          }
+          at = end;
+          if (++t == q.tiles) {
+            t = 0;
+            if (++h == p.Hkv) {
+              h = 0;
+              do {
+                if (++s >= p.n_seq) break;
+                q = span(s);
+              } while (q.tiles == 0);
+              if (s >= p.n_seq) break;
+            }
+          }
+        }
+      }
+    }
+    if (ok) {
+      SeqSpan q{};
+      SeqItem it{};
+      ok = put(-1, q, 0, it, 0, 0);  // the end
+    }
+    if (!ok && lane == 0) fail();
+  } else if (warp == C::WARP_LOAD) {
+    // ======================= TMA producer ==================================
+    if (lane == 0) {
+      ptx::prefetch_tmap(&tmQ);
+      ptx::prefetch_tmap(&tmK);
+      ptx::prefetch_tmap(&tmV);
+    }
+    const int nch = C::BK / p.chunk;
+    const int q_box_rows = p.g * p.rt;
+    uint32_t ring = 0;   // loads issued
+    uint32_t tails = 0;  // cleared last blocks
+    bool ok = true;
+    bool last_tail = false;
+    int q_loads = 0;
+    SeqRecord it;
+    for (int n = 0; ok; ++n) {
+      ok = __all_sync(0xffffffffu, next_item(n, it)) != 0;
+      if (!ok) break;
+      if (lane == 0) item_read(n);
+      if (it.seq < 0) break;
+      const int nb = it.nb;
+      const int nload = 2 * nb;
+      const int q_at = n == 0 ? 0 : (nb >= 2 ? 3 : min(1, nload));
+      for (int r = 0; r <= nload && ok; ++r) {
+        if (r == q_at) {
+          // Q, once the item before has finished with it (its first K and V
+          // do not wait for that)
+          if (lane == 0) {
+            if (n > 0)
+              ok = ptx::mbar_wait(bar(C::B_DONE), (n - 1) & 1, abort_flag, p.timeout_ns);
+            if (ok) {
+              const int tiles = it.one() ? 1 : 2;
+              ptx::mbar_arrive_expect_tx(bar(C::B_Q), tiles * C::DBOX * q_box_rows * 128);
+              for (int i = 0; i < tiles; ++i)
+#pragma unroll
+                for (int x = 0; x < C::DBOX; ++x)
+                  ptx::tma_load_4d(sb + C::OFF_Q + i * C::TILE + x * C::BOX, &tmQ, x * 64, 0,
+                                   it.qtok + i * p.rt, it.hk, bar(C::B_Q));
+              q_loads = n + 1;
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        }
+        if (r == nload || !ok) break;
+        // the order in which the issuer takes the blocks
+        bool is_v;
+        int b;
+        if (!it.one()) {
+          is_v = r & 1;
+          b = r >> 1;
+        } else if (r < 2 && r < nb) {
+          is_v = false;
+          b = r;
+        } else if (r == nload - 1) {
+          is_v = true;
+          b = nb - 1;
+        } else {
+          is_v = (r & 1) == 0;
+          b = is_v ? (r - 2) >> 1 : (r + 1) >> 1;
+        }
+        const int key0 = (it.b0 + b) * C::BK;
+        const int valid = min(C::BK, it.kvlen - key0);
+        // this lane's piece of the block
+        int row = it.k0 + key0, page = 0;
+        const bool mine = lane < nch && lane * p.chunk < valid;
+        if (p.table && mine) {
+          const int key = key0 + lane * p.chunk;
+          row = key % p.page_size;
+          page = p.table[static_cast<long long>(it.seq) * p.table_stride + key / p.page_size];
+          if (page < 0 || page >= p.n_pages) {
+            seq_record_error(p.err, BLASST_EINDEX);
+            page = p.n_pages;  // outside the map: zeros
+          }
+        }
+        const uint32_t st = ring % C::NST;
+        const uint32_t full = bar(C::B_KVF + st);
+        const bool tail = is_v && valid < C::BK;
+        const uint32_t fb = tail ? bar(C::B_TAIL) : full;
+        if (lane == 0) {
+          if (ring >= C::NST)
+            ok = ptx::mbar_wait(bar(C::B_KVE + st), ((ring / C::NST) - 1) & 1, abort_flag,
+                                p.timeout_ns);
+          if (ok) {
+            const int pieces = (valid + p.chunk - 1) / p.chunk;
+            ptx::mbar_arrive_expect_tx(fb, pieces * p.chunk * 128 * C::DBOX);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        const uint32_t dst = sb + C::OFF_KV + st * C::TILE;
+        if (mine) {
+          const CUtensorMap* tm = is_v ? &tmV : &tmK;
+#pragma unroll
+          for (int x = 0; x < C::DBOX; ++x)
+            ptx::tma_load_4d(dst + x * C::BOX + lane * p.chunk * 128, tm, x * 64, row, it.hk, page, fb);
+        }
+        ++ring;
+        last_tail = tail;
+        if (tail) {
+          // Rows behind the sequence's end (a neighbour's, a page's leftovers,
+          // an earlier block's) may hold anything, and 0 x NaN is NaN: clear
+          // them. K needs no clearing, its scores are replaced.
+          ok = ptx::mbar_wait(bar(C::B_TAIL), tails & 1, abort_flag, p.timeout_ns);
+          ok = __all_sync(0xffffffffu, ok) != 0;
+          ++tails;
+          if (!ok) break;
+          for (int i = valid * 8 + lane; i < C::BK * 8; i += 32)
+#pragma unroll
+            for (int x = 0; x < C::DBOX; ++x)
+              *reinterpret_cast<uint4*>(smem + C::OFF_KV + st * C::TILE + x * C::BOX + i * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(full);
+          last_tail = false;
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      fail();
+      // copies in flight land before the CTA exits (1 ms each is ample)
+      const uint64_t drain_ns = p.timeout_ns < 1000000ull ? p.timeout_ns : 1000000ull;
+      for (uint32_t k = ring < C::NST ? 0 : ring - C::NST; k < ring; ++k)
+        if (!(last_tail && k + 1 == ring))
+          ptx::mbar_wait(bar(C::B_KVF + k % C::NST), (k / C::NST) & 1, &misc[3], drain_ns);
+      if (last_tail) ptx::mbar_wait(bar(C::B_TAIL), (tails - 1) & 1, &misc[3], drain_ns);
+      if (q_loads > 0) ptx::mbar_wait(bar(C::B_Q), (q_loads - 1) & 1, &misc[3], drain_ns);
+    }
+  } else if (warp == C::WARP_MMA) {
+    // ======================= tcgen05 issuer ================================
+    if (lane == 0) {
+      bool ok = true;
+      const uint64_t q_desc = ptx::sw128_desc(sb + C::OFF_Q, 16, 1024);
+      const uint64_t k_desc = ptx::sw128_desc(sb + C::OFF_KV, 16, 1024);
+      const uint64_t v_desc = ptx::sw128_desc(sb + C::OFF_KV, C::BOX, 1024);
+      uint32_t ring0 = 0;                 // ring position of the item's first load
+      uint32_t steps[2] = {0, 0};         // blocks done per stream (P phases)
+      SeqRecord it;
+      for (int n = 0; ok; ++n) {
+        ok = next_item(n, it);
+        if (!ok) break;
+        item_read(n);
+        if (it.seq < 0) break;
+        const int nb = it.nb;
+        const bool one = it.one();
+        const int cnt[2] = {it.cnt(0), it.cnt(1)};
+        ok = ptx::mbar_wait(bar(C::B_Q), n & 1, abort_flag, p.timeout_ns);
+        if (!ok) break;
+        auto issue_s = [&](int st, int i) -> bool {
+          const int b = one ? 2 * i + st : i;
+          const uint32_t k = ring0 + (one ? (b < 2 ? b : 2 * b - 1) : 2 * b);
+          const uint32_t slot = k % C::NST;
+          if (!ptx::mbar_wait(bar(C::B_KVF + slot), (k / C::NST) & 1, abort_flag, p.timeout_ns))
+            return false;
+          ptx::tc_fence_after();
+          const uint64_t qd =
+              q_desc + static_cast<uint64_t>(one ? 0 : st * (C::TILE >> 4));
+          const uint64_t kd = k_desc + static_cast<uint64_t>(slot * (C::TILE >> 4));
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t o = static_cast<uint64_t>(((kk >> 2) * C::BOX + (kk & 3) * 32) >> 4);
+            ptx::mma_ss(tmem + C::S_COL + st * 128, qd + o, kd + o, IDESC_S, kk > 0 ? 1u : 0u);
+          }
+          ptx::mma_commit(bar(C::B_S + st));
+          if (one || st == 1) ptx::mma_commit(bar(C::B_KVE + slot));
+          return true;
+        };
+        auto issue_pv = [&](int st, int i) -> bool {
+          const int b = one ? 2 * i + st : i;
+          const uint32_t k =
+              ring0 + (one ? (b == nb - 1 ? 2 * nb - 1 : 2 * b + 2) : 2 * b + 1);
+          const uint32_t slot = k % C::NST;
+          if (!ptx::mbar_wait(bar(C::B_P + st), steps[st] & 1, abort_flag, p.timeout_ns))
+            return false;
+          ++steps[st];
+          if (!ptx::mbar_wait(bar(C::B_KVF + slot), (k / C::NST) & 1, abort_flag, p.timeout_ns))
+            return false;
+          ptx::tc_fence_after();
+          const uint64_t vd = v_desc + static_cast<uint64_t>(slot * (C::TILE >> 4));
+          const uint32_t o_tm = tmem + C::O_COL + st * D;
+          const uint32_t p_tm = tmem + C::S_COL + st * 128;
+          ptx::mma_ts(o_tm, p_tm, vd, IDESC_PV, i > 0 ? 1u : 0u);
+#pragma unroll
+          for (int kk = 1; kk < C::BK / 16; ++kk)
+            ptx::mma_ts(o_tm, p_tm + kk * 8, vd + static_cast<uint64_t>(kk * (2048 >> 4)), IDESC_PV,
+                        1u);
+          if (one || st == 1) ptx::mma_commit(bar(C::B_KVE + slot));
+          return true;
+        };
+        for (int st = 0; st < 2 && ok; ++st)
+          if (cnt[st] > 0) ok = issue_s(st, 0);
+        // O is free once the item before has been read out
+        if (ok && n > 0) ok = ptx::mbar_wait(bar(C::B_OFREE), (n - 1) & 1, abort_flag, p.timeout_ns);
+        const int most = max(cnt[0], cnt[1]);
+        for (int i = 0; i < most && ok; ++i)
+          for (int st = 0; st < 2 && ok; ++st) {
+            if (i < cnt[st]) ok = issue_pv(st, i);
+            if (ok && i + 1 < cnt[st]) ok = issue_s(st, i + 1);
+          }
+        ptx::mma_commit(bar(C::B_DONE));
+        ring0 += 2 * nb;
+      }
+      if (!ok) fail();
+      // every product has completed before TMEM is freed
+      ptx::mma_commit(bar(C::B_DRAIN));
+      ptx::mbar_wait(bar(C::B_DRAIN), 0, &misc[3], p.timeout_ns);
+    }
+   }
+  } else {
+    ptx::reg_take<C::REGS_SOFT>();
+    // ======================= softmax =======================================
+    const int st = warp >> 2;
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;  // row of the tile, TMEM lane
+    const int row_tok = row / p.g, row_head = row % p.g;
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t s_tm = tmem + lane_base + C::S_COL + st * 128;
+    const uint32_t o_tm = tmem + lane_base + C::O_COL + st * D;
+    const float sl2 = p.scale_log2;
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    uint32_t steps = 0;  // blocks done (S phases)
+    uint32_t ones = 0;   // one-tile items done
+    bool ok = true;
+    auto lane0_wait = [&](uint32_t b, uint32_t parity) -> bool {
+      bool r = true;
+      if (lane == 0) r = ptx::mbar_wait(b, parity, abort_flag, p.timeout_ns);
+      return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
+    };
+    SeqRecord it;
+    for (int n = 0; ok; ++n) {
+      ok = __all_sync(0xffffffffu, next_item(n, it)) != 0;
+      if (!ok) break;
+      if (lane == 0) item_read(n);
+      if (it.seq < 0) break;
+      const bool one = it.one();
+      const int cnt = it.cnt(st);
+      const int first_tok = one ? 0 : st * p.rt;
+      const int tok = first_tok + row_tok;  // of the item
+      const bool exists = row_tok < p.rt && tok < it.ntok;
+      const bool active = __any_sync(0xffffffffu, exists) != 0;
+      // keys below `limit` are visible; the tile's first token sees the fewest
+      const int limit = p.causal ? min(it.vis + tok, it.kvlen) : it.kvlen;
+      const int least = p.causal ? min(it.vis + first_tok, it.kvlen) : it.kvlen;
+      float mref = -INFINITY, l = 0.0f;
+      for (int i = 0; i < cnt; ++i) {
+        const int col0 = (it.b0 + (one ? 2 * i + st : i)) * C::BK;
+        ok = lane0_wait(bar(C::B_S + st), steps & 1);
+        ++steps;
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (active) {
+          uint32_t sv[128];
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          const bool cut = col0 + C::BK > least;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) ptx::tmem_ld32p(s_tm + 32 * c, sv + 32 * c);
+          ptx::tmem_wait_ld();
+          if (cut) {
+            const int vis = limit - col0;
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c >= vis) sv[c] = __float_as_uint(-INFINITY);
+          }
+#pragma unroll
+          for (int c = 0; c < 128; c += 8) {
+            mx[0] = ptx::fmax3(mx[0], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+            mx[1] = ptx::fmax3(mx[1], __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+            mx[2] = ptx::fmax3(mx[2], __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
+            mx[3] = ptx::fmax3(mx[3], __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
+          }
+          const float mb = fmaxf(ptx::fmax3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
+          const bool need = mb > mref + C::TAU;  // the first keys of a row always move it
+          if (__any_sync(0xffffffffu, need)) {
+            const float mnew = need ? mb : mref;
+            const float alpha = need ? ptx::ex2(mref - mnew) : 1.0f;  // 0 from -inf
+            mref = mnew;
+            l *= alpha;
+            if (i > 0) {
+              // S of this block was issued behind the P V of the one before:
+              // O is quiet until P is handed on
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t r[32];
+                ptx::tmem_ld32(o_tm + 32 * c, r);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+                ptx::tmem_st32(o_tm + 32 * c, r);
+              }
+            }
+          }
+          const float neg = mref == -INFINITY ? 0.0f : -mref;
+          float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              float x0, x1;
+              ptx::fma2(x0, x1, __uint_as_float(sv[32 * c + j]), __uint_as_float(sv[32 * c + j + 1]),
+                        sl2, sl2, neg, neg);
+              const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+              const int a = j & 6;
+              ptx::add2(rs[a], rs[a + 1], rs[a], rs[a + 1], p0, p1);
+              pk[j / 2] = seq_pack2<T>(p0, p1);
+            }
+            ptx::tmem_st16(s_tm + 16 * c, pk);
+          }
+          l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+          ptx::tmem_wait_st();
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_P + st));
+      }
+
+      // ---- the item's end ---------------------------------------------------
+      if (!ok) break;
+      float w0 = 1.0f, w1 = 0.0f;
+      if (one) {
+        // (the item before has been read out by all warps: ml may be written)
+        if (n > 0) ok = lane0_wait(bar(C::B_OFREE), (n - 1) & 1);
+        ml[st * 128 + row] = make_float2(mref, l);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_ML));
+        ok = lane0_wait(bar(C::B_ML), ones & 1) && ok;
+        ++ones;
+        if (!ok) break;
+        const float2 a = ml[row], c = ml[128 + row];
+        mref = fmaxf(a.x, c.x);
+        w0 = a.x == -INFINITY ? 0.0f : ptx::ex2(a.x - mref);
+        w1 = c.x == -INFINITY ? 0.0f : ptx::ex2(c.x - mref);
+        l = a.y * w0 + c.y * w1;
+      }
+      ok = lane0_wait(bar(C::B_DONE), n & 1);
+      ok = ok && *abort_flag == 0;
+      ok = __all_sync(0xffffffffu, ok) != 0;
+      if (!ok) break;
+      ptx::tc_fence_after();
+      // 0 where the row saw no key; NaN (from NaN inputs) stays
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float lse2 = l == 0.0f ? -INFINITY : mref + log2f(l);
+      const bool whole = it.mode & SeqRecord::kWhole;
+      const long long tok_row = static_cast<long long>(it.qtok + tok) * p.Hq + it.hk * p.g + row_head;
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (it.mode & SeqRecord::kBegins ? 1 : 0);
+      const int prow = (one ? 0 : st * 128) + row;
+      // one tile: each warpgroup takes half of the columns of both sums
+      const int c_lo = one ? st * (D / 64) : 0;
+      const int c_hi = one ? c_lo + D / 64 : D / 32;
+      const bool second = one && it.nb > 1;
+      if (active) {
+#pragma unroll 1
+        for (int c = c_lo; c < c_hi; ++c) {
+          uint32_t r[32];
+          if (cnt > 0 || one) {
+            ptx::tmem_ld32(tmem + lane_base + C::O_COL + (one ? 0 : st * D) + 32 * c, r);
+            ptx::tmem_wait_ld();
+          }
+          if (second) {
+            uint32_t r2[32];
+            ptx::tmem_ld32(tmem + lane_base + C::O_COL + D + 32 * c, r2);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              r[j] = __float_as_uint(w0 * __uint_as_float(r[j]) + w1 * __uint_as_float(r2[j]));
+          } else if (one) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(w0 * __uint_as_float(r[j]));
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            r[j] = l == 0.0f ? 0u : __float_as_uint(__uint_as_float(r[j]) * inv);
+          if (exists) {
+            if (whole) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + tok_row * D + 32 * c);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  w[k] = seq_pack2<T>(__uint_as_float(r[8 * j + 2 * k]),
+                                      __uint_as_float(r[8 * j + 2 * k + 1]));
+                dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(
+                  p.part_o + (static_cast<size_t>(slot) * 256 + prow) * D + 32 * c);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                dst[j] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+            }
+          }
+        }
+      }
+      if (exists && (st == 0 || !one)) {
+        if (whole) p.lse[tok_row] = lse2 * 0.6931471805599453f;
+        else p.part_lse[static_cast<size_t>(slot) * 256 + prow] = lse2;
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(C::B_OFREE));
+    }
+    if (!ok) fail();
+  }
+
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == C::WARP_MMA) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Joins the partials of the items that ranges cut: CTA c looks after the item
+// that begins in range c and goes on behind it. o = sum_i w_i o_i / sum_i w_i,
+// w_i = 2^(lse_i - max), in the order of the ranges.
+template <int D, typename T>
+__global__ void __launch_bounds__(256) blasst_seq_join_kernel(const SeqAttnParams p) {
+  const int c = blockIdx.x;
+  const int4 d = p.part_desc[2 * c];
+  if (d.x < 0) return;
+  const int last = p.part_desc[2 * c + 1].x;
+  const int lane = threadIdx.x & 31;
+  constexpr int V = D / 32;  // columns per lane
+  const int rows = d.w ? 128 : 256;
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
+    const int tok = (r >> 7) * p.rt + (r & 127) / p.g;
+    if ((r & 127) >= p.g * p.rt || tok >= d.y) continue;
+    float m = -INFINITY, l = 0.0f, acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+    for (int k = c; k <= last; ++k) {
+      const size_t row = static_cast<size_t>(2 * k + (k == c ? 1 : 0)) * 256 + r;
+      const float x = p.part_lse[row];
+      const float* src = p.part_o + row * D + lane * V;
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[v] = src[v];
+      if (x == -INFINITY) continue;
+      const float mn = fmaxf(m, x);
+      const float a = m == -INFINITY ? 0.0f : ptx::ex2(m - mn), w = ptx::ex2(x - mn);
+      m = mn;
+      l = l * a + w;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = acc[v] * a + w * o[v];
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const long long out = static_cast<long long>(d.x + tok) * p.Hq + d.z * p.g + (r & 127) % p.g;
+    uint32_t w2[V / 2];
+#pragma unroll
+    for (int v = 0; v < V / 2; ++v) w2[v] = seq_pack2<T>(acc[2 * v] * inv, acc[2 * v + 1] * inv);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.o) + out * D) + lane * (V / 2);
+#pragma unroll
+    for (int v = 0; v < V / 2; ++v) dst[v] = w2[v];
+    if (lane == 0) p.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+}  // namespace blasst

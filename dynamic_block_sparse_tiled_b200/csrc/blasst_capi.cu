@@ -1,8 +1,9 @@
 // blasst_capi.cu - the exported C ABI (include/blasst.h): argument checks,
 // TMA tensor maps, kernel selection and launch, the device error word.
 //
-// Single translation unit: the kernels are included here so that the error
-// word and every template instantiation live in one module.
+// The kernels of the dense operators are included here; those over sequences
+// of different lengths are in blasst_seq_capi.cu, which shares the error word
+// through capi_internal.h.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -16,6 +17,7 @@
 
 #include "../../include/blasst.h"
 #include "bwd_sm100.cuh"
+#include "capi_internal.h"
 #include "decode_mla_sm100.cuh"
 #include "decode_sm100.cuh"
 #include "prefill_f32_sm100.cuh"
@@ -29,7 +31,7 @@ namespace {
 __device__ int g_blasst_error = 0;
 
 constexpr int kMaxDevices = 64;
-constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per bounded wait
+using blasst::capi::kTimeoutNs;
 
 std::mutex g_mu;
 int* g_err_ptr[kMaxDevices] = {nullptr};
@@ -237,6 +239,14 @@ float log2_lambda_of(float lambda) {
 
 }  // namespace
 
+namespace blasst {
+namespace capi {
+int* error_word() { return ::error_word(); }
+PFN_cuTensorMapEncodeTiled_v12000 encoder() { return ::encoder(); }
+int cuda_status(cudaError_t e) { return ::cuda_status(e); }
+}  // namespace capi
+}  // namespace blasst
+
 extern "C" {
 
 int blasst_version(void) { return 100; }
@@ -251,6 +261,7 @@ const char* blasst_status_string(int status) {
     case BLASST_ECUDA: return "BLASST_ECUDA: CUDA call failed";
     case BLASST_ETIMEOUT: return "BLASST_ETIMEOUT: a device-side bounded wait gave up";
     case BLASST_EWORKSPACE: return "BLASST_EWORKSPACE: workspace missing or too small";
+    case BLASST_EINDEX: return "BLASST_EINDEX: a device-side length, offset or page number is out of range";
     default: return "BLASST: unknown status";
   }
 }

@@ -1,0 +1,422 @@
+// blasst_seq_capi.cu - C ABI of the operators over sequences of different
+// lengths (include/blasst.h): argument checks, tensor maps, launch rules.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/blasst.h"
+#include "attn_seq_sm100.cuh"
+#include "capi_internal.h"
+#include "rotary_sm100.cuh"
+
+namespace {
+
+using blasst::capi::cuda_status;
+using blasst::capi::encoder;
+using blasst::capi::error_word;
+using blasst::capi::kTimeoutNs;
+
+constexpr int kMaxDevices = 64;
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// SMs of the current device (a host-side query, kept per device).
+int sm_count() {
+  static int known[kMaxDevices] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  if (dev < kMaxDevices && known[dev] > 0) return known[dev];
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < kMaxDevices) known[dev] = n;
+  return n;
+}
+
+// 4-D map (d, rows, heads or groups, outer), 128-byte swizzle, zero fill
+// outside. Strides in elements of 2 bytes.
+bool make_map4(CUtensorMap* map, const void* base, int dtype, const long long (&dim)[4],
+               const long long (&stride)[3], int box1, int box2) {
+  auto enc = encoder();
+  if (!enc) return false;
+  cuuint64_t dims[4], strides[3];
+  for (int i = 0; i < 4; ++i) dims[i] = static_cast<cuuint64_t>(dim[i] > 0 ? dim[i] : 1);
+  // the stride of a dimension of one entry is never used, but has to be valid
+  for (int i = 0; i < 3; ++i)
+    strides[i] = dims[i + 1] == 1 ? 16 : static_cast<cuuint64_t>(stride[i]) * 2;
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const auto dt = dtype == BLASST_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return enc(map, dt, 4, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A stride a tensor map can hold: positive, a multiple of 16 bytes, < 2^40.
+bool map_stride(long long elems) { return elems > 0 && elems % 8 == 0 && elems < (1ll << 39); }
+
+size_t seq_workspace(int sms, int d) {
+  return static_cast<size_t>(sms) * (2 * 256 * (static_cast<size_t>(d) + 1) * 4 + 32);
+}
+
+// The register split of a kernel waits for registers the launch must have:
+// refused (not run) if a build gave the kernel fewer.
+template <typename K>
+int check_regs(K kernel, int regs, int& known) {
+  if (known == 0) {
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return cuda_status(e);
+    known = fa.numRegs;
+  }
+  return known >= regs ? BLASST_OK : BLASST_EUNSUPPORTED;
+}
+
+template <int D, typename T>
+int launch_seq(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+               const blasst::SeqAttnParams& p, int sms, cudaStream_t stream) {
+  using C = blasst::SeqAttnCfg<D>;
+  auto kernel = blasst::blasst_seq_attn_kernel<D, T>;
+  static int regs = 0;  // of this instantiation
+  if (const int rc = check_regs(kernel, C::REGS, regs)) return rc;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return cuda_status(e);
+  const bool shared_list = p.n_tiles == 0;
+  const unsigned grid =
+      shared_list ? static_cast<unsigned>(sms) : static_cast<unsigned>(p.n_tiles) * p.Hkv;
+  kernel<<<grid, C::NTHREADS, C::SMEM_BYTES, stream>>>(mq, mk, mv, p);
+  int rc = cuda_status(cudaGetLastError());
+  if (rc != BLASST_OK || !shared_list) return rc;
+  blasst::blasst_seq_join_kernel<D, T><<<dim3(grid, 4), 256, 0, stream>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+// What the packed and the paged call share; `p` holds the keys' side already.
+int run_seq(blasst::SeqAttnParams& p, const void* q, long long q_st, long long q_sh, int d,
+            float scale, int dtype, const CUtensorMap& mk, const CUtensorMap& mv, void* workspace,
+            int sms, void* stream) {
+  p.rt = 128 / p.g;
+  // One item per CTA once the tiles fill the GPU several times: their order
+  // then shares K and V in L2. Fewer tiles, or mostly single tokens: the
+  // shared list, which cuts long rows of key blocks between SMs.
+  const long long full = static_cast<long long>(p.Tq) / (2 * p.rt);
+  const long long tiles = std::min<long long>(p.Tq, full + p.n_seq);
+  p.n_tiles = full * p.Hkv >= 8ll * sms && tiles * p.Hkv < 0x7fffffffll ? static_cast<int>(tiles) : 0;
+  const size_t rows = static_cast<size_t>(sms) * 2 * 256;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = p.part_o + rows * d;
+  p.part_desc = reinterpret_cast<int4*>(p.part_lse + rows);
+  const double sc = scale > 0.0f ? static_cast<double>(scale) : 1.0 / std::sqrt(static_cast<double>(d));
+  p.scale_log2 = static_cast<float>(sc * 1.4426950408889634);
+  p.timeout_ns = kTimeoutNs;
+  CUtensorMap mq;
+  if (!make_map4(&mq, q, dtype, {d, p.g, p.Tq, p.Hkv}, {q_sh, q_st, q_sh * p.g}, p.g, p.rt))
+    return BLASST_ECUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == BLASST_BF16)
+    return d == 128 ? launch_seq<128, __nv_bfloat16>(mq, mk, mv, p, sms, s)
+                    : launch_seq<64, __nv_bfloat16>(mq, mk, mv, p, sms, s);
+  return d == 128 ? launch_seq<128, __half>(mq, mk, mv, p, sms, s)
+                  : launch_seq<64, __half>(mq, mk, mv, p, sms, s);
+}
+
+int check_heads(int n_seq, int Tq, int Hq, int Hkv, int d, int dtype) {
+  if (n_seq < 0 || Tq < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return BLASST_EINVAL;
+  if (Hkv > 65535 || n_seq > (1 << 24)) return BLASST_EINVAL;
+  if (d != 64 && d != 128) return BLASST_EUNSUPPORTED;
+  if (Hq / Hkv > 128) return BLASST_EUNSUPPORTED;
+  if (dtype != BLASST_BF16 && dtype != BLASST_FP16) return BLASST_EUNSUPPORTED;
+  return BLASST_OK;
+}
+
+int elem_bytes(int dtype) { return dtype == BLASST_FP32 ? 4 : 2; }
+
+// Widest vector (elements) that both sides' base and strides allow.
+bool vector_ok(const void* p, const long long* strides, int n, int vec, int bytes) {
+  if (!aligned(p, static_cast<uintptr_t>(vec) * bytes)) return false;
+  for (int i = 0; i < n; ++i)
+    if (strides[i] % vec != 0) return false;
+  return true;
+}
+
+bool rotary_vec(int d, int rot, bool interleaved, int vec) {
+  if (interleaved) return d % vec == 0 && rot % vec == 0;
+  return (rot / 2) % vec == 0 && (d - rot) % vec == 0;
+}
+
+template <typename T, int VEC>
+int launch_rotary(const blasst::RotaryParams& p, dim3 grid, size_t smem, cudaStream_t s) {
+  blasst::blasst_rotary_kernel<T, VEC><<<grid, 256, smem, s>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+template <typename T, int VEC>
+int launch_append(const blasst::AppendParams& p, dim3 grid, size_t smem, cudaStream_t s) {
+  blasst::blasst_append_kernel<T, VEC><<<grid, 256, smem, s>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+// Heads per block: all of them, unless few tokens would leave SMs idle.
+int heads_per_block(long long blocks, int heads, int places, int sms) {
+  const int groups = std::max(1, 256 / std::min(places, 256));
+  int split = 1;
+  while (blocks * split < 2ll * sms && heads > groups * split) split *= 2;
+  return (heads + split - 1) / split;
+}
+
+}  // namespace
+
+extern "C" {
+
+int blasst_rotary(const blasst_rotary_args* a) {
+  if (!a || !a->x || !a->y || !a->freq) return BLASST_EINVAL;
+  if (a->dtype != BLASST_BF16 && a->dtype != BLASST_FP16 && a->dtype != BLASST_FP32)
+    return BLASST_EUNSUPPORTED;
+  const int eb = elem_bytes(a->dtype);
+  if (a->B < 0 || a->L < 0 || a->H < 0 || a->d <= 0 || a->rot < 2 || a->rot > a->d ||
+      a->rot % 2 != 0)
+    return BLASST_EINVAL;
+  if (!(a->scale > 0.0f) || !std::isfinite(a->scale)) return BLASST_EINVAL;
+  if (a->d > 1024) return BLASST_EUNSUPPORTED;
+  if (!aligned(a->x, eb) || !aligned(a->y, eb) || !aligned(a->freq, 8) ||
+      (a->positions && !aligned(a->positions, a->pos64 ? 8 : 4)))
+    return BLASST_EINVAL;
+  // the same elements by other strides would be read after they are written
+  if (a->x == a->y && (a->x_sb != a->y_sb || a->x_sl != a->y_sl || a->x_sh != a->y_sh))
+    return BLASST_EINVAL;
+  const long long tokens = static_cast<long long>(a->B) * a->L;
+  if (tokens == 0 || a->H == 0) return BLASST_OK;
+  const int sms = sm_count();
+  if (sms == 0) return BLASST_ECUDA;
+  blasst::RotaryParams p{};
+  p.x = a->x;
+  p.y = a->y;
+  p.pos = a->positions;
+  p.freq = a->freq;
+  p.x_sb = a->x_sb;
+  p.x_st = a->x_sl;
+  p.x_sh = a->x_sh;
+  p.y_sb = a->y_sb;
+  p.y_st = a->y_sl;
+  p.y_sh = a->y_sh;
+  p.pos_sb = a->pos_sb;
+  p.pos64 = a->pos64;
+  p.B = a->B;
+  p.L = a->L;
+  p.H = a->H;
+  p.d = a->d;
+  p.rot = a->rot;
+  p.interleaved = a->interleaved ? 1 : 0;
+  p.sign = a->inverse ? -1.0f : 1.0f;
+  p.mscale = a->scale;
+  const int vec = 16 / eb;
+  const long long sx[3] = {a->x_sb, a->x_sl, a->x_sh}, sy[3] = {a->y_sb, a->y_sl, a->y_sh};
+  const bool wide = rotary_vec(a->d, a->rot, p.interleaved, vec) &&
+                    vector_ok(a->x, sx, 3, vec, eb) && vector_ok(a->y, sy, 3, vec, eb);
+  const int places = blasst::rotary_places(a->d, a->rot, p.interleaved, wide ? vec : 1);
+  // four tokens per block share the set-up when there are enough of them
+  p.tb = tokens >= 16ll * sms ? 4 : 1;
+  const long long blocks = (tokens + p.tb - 1) / p.tb;
+  if (blocks > 0x7fffffffll) return BLASST_EINVAL;
+  p.hb = heads_per_block(blocks, a->H, places, sms);
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((a->H + p.hb - 1) / p.hb));
+  if (grid.y > 65535) return BLASST_EINVAL;
+  const size_t smem = static_cast<size_t>(p.tb) * (a->rot / 2) * sizeof(float2);
+  const cudaStream_t s = static_cast<cudaStream_t>(a->stream);
+  if (a->dtype == BLASST_BF16)
+    return wide ? launch_rotary<__nv_bfloat16, 8>(p, grid, smem, s)
+                : launch_rotary<__nv_bfloat16, 1>(p, grid, smem, s);
+  if (a->dtype == BLASST_FP16)
+    return wide ? launch_rotary<__half, 8>(p, grid, smem, s)
+                : launch_rotary<__half, 1>(p, grid, smem, s);
+  return wide ? launch_rotary<float, 4>(p, grid, smem, s) : launch_rotary<float, 1>(p, grid, smem, s);
+}
+
+int blasst_append(const blasst_append_args* a) {
+  if (!a || !a->k || !a->v || !a->k_pages || !a->v_pages || !a->page_table || !a->kv_lens ||
+      !a->cu_q || (a->q == nullptr) != (a->q_out == nullptr))
+    return BLASST_EINVAL;
+  if (a->dtype != BLASST_BF16 && a->dtype != BLASST_FP16 && a->dtype != BLASST_FP32)
+    return BLASST_EUNSUPPORTED;
+  if (a->n_seq < 0 || a->T < 0 || a->Hkv <= 0 || (a->q && a->Hq <= 0) || a->d <= 0 ||
+      a->n_pages <= 0 || a->page_size <= 0 || a->table_width < 0 ||
+      a->table_stride < a->table_width)
+    return BLASST_EINVAL;
+  if (a->freq ? (a->rot < 2 || a->rot > a->d || a->rot % 2 != 0) : a->rot != 0) return BLASST_EINVAL;
+  if (a->freq && (!(a->scale > 0.0f) || !std::isfinite(a->scale))) return BLASST_EINVAL;
+  if (a->d > 1024) return BLASST_EUNSUPPORTED;
+  const int eb = elem_bytes(a->dtype);
+  for (const void* ptr : {a->q, static_cast<const void*>(a->q_out), a->k, a->v,
+                          static_cast<const void*>(a->k_pages), static_cast<const void*>(a->v_pages)})
+    if (!aligned(ptr, eb)) return BLASST_EINVAL;
+  if (!aligned(a->page_table, 4) || !aligned(a->kv_lens, 4) || !aligned(a->cu_q, 4) ||
+      !aligned(a->freq, 8))
+    return BLASST_EINVAL;
+  if (a->q && a->q == a->q_out && (a->q_st != a->qo_st || a->q_sh != a->qo_sh)) return BLASST_EINVAL;
+  if (a->T == 0 || a->n_seq == 0) return BLASST_OK;
+  const int sms = sm_count();
+  int* err = error_word();
+  if (!err || sms == 0) return BLASST_ECUDA;
+  blasst::AppendParams p{};
+  p.q = a->q;
+  p.k = a->k;
+  p.v = a->v;
+  p.q_out = a->q_out;
+  p.k_pages = a->k_pages;
+  p.v_pages = a->v_pages;
+  p.q_st = a->q_st;
+  p.q_sh = a->q_sh;
+  p.k_st = a->k_st;
+  p.k_sh = a->k_sh;
+  p.v_st = a->v_st;
+  p.v_sh = a->v_sh;
+  p.qo_st = a->qo_st;
+  p.qo_sh = a->qo_sh;
+  p.kp_sp = a->kp_sp;
+  p.kp_st = a->kp_st;
+  p.kp_sh = a->kp_sh;
+  p.vp_sp = a->vp_sp;
+  p.vp_st = a->vp_st;
+  p.vp_sh = a->vp_sh;
+  p.table = a->page_table;
+  p.table_stride = a->table_stride;
+  p.table_width = a->table_width;
+  p.page_size = a->page_size;
+  p.n_pages = a->n_pages;
+  p.kv_lens = a->kv_lens;
+  p.cu_q = a->cu_q;
+  p.n_seq = a->n_seq;
+  p.T = a->T;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.d = a->d;
+  p.rot = a->rot;
+  p.interleaved = a->interleaved ? 1 : 0;
+  p.freq = a->freq;
+  p.mscale = a->scale;
+  p.err = err;
+  const int vec = 16 / eb;
+  const long long sq[4] = {a->q_st, a->q_sh, a->qo_st, a->qo_sh};
+  const long long sk[5] = {a->k_st, a->k_sh, a->kp_sp, a->kp_st, a->kp_sh};
+  const long long sv[5] = {a->v_st, a->v_sh, a->vp_sp, a->vp_st, a->vp_sh};
+  bool wide = rotary_vec(a->d, a->rot, p.interleaved, vec) && vector_ok(a->k, sk, 5, vec, eb) &&
+              vector_ok(a->k_pages, sk, 5, vec, eb) && vector_ok(a->v, sv, 5, vec, eb) &&
+              vector_ok(a->v_pages, sv, 5, vec, eb);
+  if (a->q) wide = wide && vector_ok(a->q, sq, 4, vec, eb) && vector_ok(a->q_out, sq, 4, vec, eb);
+  const int places = blasst::rotary_places(a->d, a->rot, p.interleaved, wide ? vec : 1);
+  const int heads = (a->q ? a->Hq : 0) + 2 * a->Hkv;
+  p.hb = heads_per_block(a->T, heads, places, sms);
+  const dim3 grid(static_cast<unsigned>(a->T), static_cast<unsigned>((heads + p.hb - 1) / p.hb));
+  if (grid.y > 65535) return BLASST_EINVAL;
+  const size_t smem = std::max<size_t>(1, a->rot / 2) * sizeof(float2);
+  const cudaStream_t s = static_cast<cudaStream_t>(a->stream);
+  if (a->dtype == BLASST_BF16)
+    return wide ? launch_append<__nv_bfloat16, 8>(p, grid, smem, s)
+                : launch_append<__nv_bfloat16, 1>(p, grid, smem, s);
+  if (a->dtype == BLASST_FP16)
+    return wide ? launch_append<__half, 8>(p, grid, smem, s)
+                : launch_append<__half, 1>(p, grid, smem, s);
+  return wide ? launch_append<float, 4>(p, grid, smem, s) : launch_append<float, 1>(p, grid, smem, s);
+}
+
+size_t blasst_seq_workspace_bytes(int d) {
+  if (d != 64 && d != 128) return 0;
+  return seq_workspace(sm_count(), d);
+}
+
+int blasst_packed_fwd(const blasst_packed_args* a) {
+  if (!a || !a->q || !a->k || !a->v || !a->o || !a->lse || !a->cu_q || !a->cu_k) return BLASST_EINVAL;
+  for (const void* ptr : {a->q, a->k, a->v, static_cast<const void*>(a->o),
+                          static_cast<const void*>(a->lse)})
+    if (!aligned(ptr, 16)) return BLASST_EINVAL;
+  if (!aligned(a->cu_q, 4) || !aligned(a->cu_k, 4)) return BLASST_EINVAL;
+  if (const int rc = check_heads(a->n_seq, a->Tq, a->Hq, a->Hkv, a->d, a->dtype)) return rc;
+  if (a->Tk < 0 || std::isnan(a->scale)) return BLASST_EINVAL;
+  for (long long st : {a->q_st, a->q_sh, a->k_st, a->k_sh, a->v_st, a->v_sh})
+    if (!map_stride(st)) return BLASST_EINVAL;
+  if (!aligned(a->workspace, 16) || !a->workspace) return BLASST_EWORKSPACE;
+  if (a->n_seq == 0 || a->Tq == 0) return BLASST_OK;
+  const int sms = sm_count();
+  if (sms == 0) return BLASST_ECUDA;
+  if (a->workspace_bytes < seq_workspace(sms, a->d)) return BLASST_EWORKSPACE;
+  blasst::SeqAttnParams p{};
+  p.err = error_word();
+  if (!p.err) return BLASST_ECUDA;
+  p.o = a->o;
+  p.lse = a->lse;
+  p.cu_q = a->cu_q;
+  p.cu_k = a->cu_k;
+  p.page_size = 1;
+  p.n_pages = 1;
+  p.chunk = 128;
+  p.n_seq = a->n_seq;
+  p.Tq = a->Tq;
+  p.Tk = a->Tk;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.g = a->Hq / a->Hkv;
+  p.causal = a->causal ? 1 : 0;
+  CUtensorMap mk, mv;
+  if (!make_map4(&mk, a->k, a->dtype, {a->d, a->Tk, a->Hkv, 1}, {a->k_st, a->k_sh, 8}, 128, 1) ||
+      !make_map4(&mv, a->v, a->dtype, {a->d, a->Tk, a->Hkv, 1}, {a->v_st, a->v_sh, 8}, 128, 1))
+    return BLASST_ECUDA;
+  return run_seq(p, a->q, a->q_st, a->q_sh, a->d, a->scale, a->dtype, mk, mv, a->workspace, sms,
+                 a->stream);
+}
+
+int blasst_paged_fwd(const blasst_paged_args* a) {
+  if (!a || !a->q || !a->k_pages || !a->v_pages || !a->o || !a->lse || !a->page_table ||
+      !a->kv_lens || !a->cu_q)
+    return BLASST_EINVAL;
+  for (const void* ptr : {a->q, a->k_pages, a->v_pages, static_cast<const void*>(a->o),
+                          static_cast<const void*>(a->lse)})
+    if (!aligned(ptr, 16)) return BLASST_EINVAL;
+  if (!aligned(a->cu_q, 4) || !aligned(a->kv_lens, 4) || !aligned(a->page_table, 4)) return BLASST_EINVAL;
+  if (const int rc = check_heads(a->n_seq, a->Tq, a->Hq, a->Hkv, a->d, a->dtype)) return rc;
+  if (a->n_pages <= 0 || a->page_size <= 0 || a->table_width < 0 ||
+      a->table_stride < a->table_width || std::isnan(a->scale))
+    return BLASST_EINVAL;
+  if (a->page_size % 8 != 0 || a->n_pages == 0x7fffffff) return BLASST_EUNSUPPORTED;
+  for (long long st : {a->q_st, a->q_sh, a->kp_sp, a->kp_st, a->kp_sh, a->vp_sp, a->vp_st, a->vp_sh})
+    if (!map_stride(st)) return BLASST_EINVAL;
+  if (!aligned(a->workspace, 16) || !a->workspace) return BLASST_EWORKSPACE;
+  if (a->n_seq == 0 || a->Tq == 0) return BLASST_OK;
+  const int sms = sm_count();
+  if (sms == 0) return BLASST_ECUDA;
+  if (a->workspace_bytes < seq_workspace(sms, a->d)) return BLASST_EWORKSPACE;
+  blasst::SeqAttnParams p{};
+  p.err = error_word();
+  if (!p.err) return BLASST_ECUDA;
+  p.o = a->o;
+  p.lse = a->lse;
+  p.cu_q = a->cu_q;
+  p.kv_lens = a->kv_lens;
+  p.table = a->page_table;
+  p.table_stride = a->table_stride;
+  p.table_width = a->table_width;
+  p.page_size = a->page_size;
+  p.n_pages = a->n_pages;
+  p.chunk = std::min(128, a->page_size & -a->page_size);
+  p.n_seq = a->n_seq;
+  p.Tq = a->Tq;
+  p.Tk = 0;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.g = a->Hq / a->Hkv;
+  p.causal = a->causal ? 1 : 0;
+  CUtensorMap mk, mv;
+  if (!make_map4(&mk, a->k_pages, a->dtype, {a->d, a->page_size, a->Hkv, a->n_pages},
+                 {a->kp_st, a->kp_sh, a->kp_sp}, p.chunk, 1) ||
+      !make_map4(&mv, a->v_pages, a->dtype, {a->d, a->page_size, a->Hkv, a->n_pages},
+                 {a->vp_st, a->vp_sh, a->vp_sp}, p.chunk, 1))
+    return BLASST_ECUDA;
+  return run_seq(p, a->q, a->q_st, a->q_sh, a->d, a->scale, a->dtype, mk, mv, a->workspace, sms,
+                 a->stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,24 @@
+// capi_internal.h - what the translation units of the C ABI share (hidden
+// symbols; defined in blasst_capi.cu).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <cstdint>
+
+namespace blasst {
+namespace capi {
+
+constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per bounded wait
+
+// The device error word's address on the current device, or null.
+int* error_word();
+// cuTensorMapEncodeTiled, or null.
+PFN_cuTensorMapEncodeTiled_v12000 encoder();
+// BLASST_OK or BLASST_ECUDA, with the error's text kept for
+// blasst_last_cuda_error().
+int cuda_status(cudaError_t e);
+
+}  // namespace capi
+}  // namespace blasst

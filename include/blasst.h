@@ -60,10 +60,12 @@ typedef enum {
   BLASST_EUNSUPPORTED = -2,  /* valid request this build does not implement */
   BLASST_ECUDA = -3,         /* a CUDA runtime/driver call failed */
   BLASST_ETIMEOUT = -4,      /* a device-side bounded wait gave up */
-  BLASST_EWORKSPACE = -5     /* workspace missing or too small */
+  BLASST_EWORKSPACE = -5,    /* workspace missing or too small */
+  BLASST_EINDEX = -6         /* a length, offset or page number in device memory is out of range */
 } blasst_status;
 
-typedef enum { BLASST_BF16 = 0, BLASST_FP32 = 1 } blasst_dtype;
+/* BLASST_FP16: the operators over sequences and the rotary ones only. */
+typedef enum { BLASST_BF16 = 0, BLASST_FP32 = 1, BLASST_FP16 = 2 } blasst_dtype;
 
 /* Telemetry counters, accumulated (atomically added) into a caller-owned
  * DEVICE struct when one is passed; the library never clears it. */
@@ -345,6 +347,150 @@ BLASST_API int blasst_decode_mla_splits(int B, int H, int L, int num_sms);
  * M = max_s lse_s. */
 BLASST_API int blasst_lse_merge(const float* o_parts, const float* lse_parts, void* o, float* lse, int n_rows,
                      int d, int num_splits, int out_dtype, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Sequences of different lengths: rotary positions, a paged KV cache, exact
+ * attention (no thresholding) over packed prompts and over the cache.
+ *
+ * Packed tokens: [T, heads, d] with a token stride and a head stride in
+ * elements (d contiguous); sequence s owns the tokens cu[s] .. cu[s+1]-1, cu a
+ * device int32 array of n_seq + 1 ascending offsets. Tokens before cu[0] or
+ * from cu[n_seq] on belong to nobody: outputs there are left as they were.
+ * Paged cache: [n_pages, page_size, Hkv, d] with page, token and head strides
+ * (so a head-major pool is read by its strides); token j of sequence s is at
+ * row j % page_size of page page_table[s][j / page_size]. Entries of the
+ * table behind a sequence's last token are not read.
+ * Lengths, offsets and page numbers live in device memory, so a captured
+ * graph can be replayed with others of them. Kernels check them: one that is
+ * out of range is clamped (nothing is read or written outside the tensors)
+ * and BLASST_EINDEX recorded in the device error word; the affected
+ * sequences' outputs are then undefined, and so are those of calls made
+ * after a timeout and before blasst_check (as for the dense calls).
+ * Pointers are 16-byte aligned (index arrays: naturally aligned); strides of
+ * the attention calls are multiples of 8 elements.
+ * ------------------------------------------------------------------------- */
+
+/* Rotary positions. Pair i of a head (i < rot / 2) turns by position * freq[i]:
+ *     y_a = scale (x_a cos - x_b sin),  y_b = scale (x_a sin + x_b cos),
+ * (a, b) = (i, i + rot / 2), or (2i, 2i + 1) when interleaved; dims from rot on
+ * are copied. inverse = 1 negates the angle: the gradient's transposed turn.
+ *   x, y       [B, L, H, d] by strides (d contiguous), B = 1 for packed
+ *              tokens. y may be x (same strides); other overlaps are invalid.
+ *   positions  device int32 (pos64 = 0) or int64, [B, L] with batch stride
+ *              pos_sb (0 for one row used by all); NULL: 0 .. L-1.
+ *   freq       device double [rot / 2], radians per position: scalings for long
+ *              contexts are in this table. Angles are formed in 64 bits.
+ *   scale      factor on the turned dims (> 0), e.g. a scaling's own.
+ *   d          1 .. 1024; rot even, 2 .. d. dtype: BF16, FP16 or FP32. */
+typedef struct blasst_rotary_args {
+  const void* x;
+  void* y;
+  const void* positions;
+  const double* freq;
+  int pos64;
+  int B, L, H, d, rot;
+  long long x_sb, x_sl, x_sh, y_sb, y_sl, y_sh, pos_sb;
+  int interleaved, inverse;
+  float scale;
+  int dtype;
+  void* stream;
+} blasst_rotary_args;
+BLASST_API int blasst_rotary(const blasst_rotary_args* args);
+
+/* Writes the new tokens' k and v into the paged cache and turns q and k on the
+ * way. kv_lens[s] counts sequence s's tokens with the new ones, so token t of
+ * the sequence (its last kv tokens are the new ones) has position
+ * kv_lens[s] - (cu_q[s+1] - t), which also gives its page and row.
+ *   q, q_out   [T, Hq, d] or NULL (both): q_out may be q.
+ *   k, v       [T, Hkv, d].
+ *   freq       as in blasst_rotary; NULL (with rot = 0): nothing is turned.
+ * Pages not named by the new tokens are not touched. A token whose place is
+ * out of range is not written (BLASST_EINDEX). Two tokens with the same place
+ * (a table that names a page twice) leave one of them there. */
+typedef struct blasst_append_args {
+  const void* q;
+  void* q_out;
+  const void* k;
+  const void* v;
+  void* k_pages;
+  void* v_pages;
+  const int* page_table;
+  const int* kv_lens;
+  const int* cu_q;
+  const double* freq;
+  int n_seq, T, Hq, Hkv, d, rot;
+  int n_pages, page_size, table_width;
+  long long table_stride;
+  long long q_st, q_sh, qo_st, qo_sh, k_st, k_sh, v_st, v_sh;
+  long long kp_sp, kp_st, kp_sh, vp_sp, vp_st, vp_sh;
+  int interleaved;
+  float scale;
+  int dtype;
+  void* stream;
+} blasst_append_args;
+BLASST_API int blasst_append(const blasst_append_args* args);
+
+/* Attention over packed sequences, exact: query token i of sequence s sees
+ * key j when j <= i + (len_k - len_q) (causal = 1, bottom-right) or every key
+ * of the sequence (causal = 0). Rows without keys get o = 0, lse = -inf.
+ *   q [Tq, Hq, d], k, v [Tk, Hkv, d] by strides; o [Tq, Hq, d] and lse
+ *   [Tq, Hq] (fp32, natural log) contiguous.
+ *   cu_q, cu_k  device int32 [n_seq + 1].
+ *   d 64 or 128; Hq a multiple of Hkv, Hq / Hkv <= 128; dtype BF16 or FP16.
+ *   scale       <= 0 selects 1/sqrt(d).
+ *   workspace   >= blasst_seq_workspace_bytes(d) bytes. Calls that may run at
+ *               the same time need workspaces of their own. */
+typedef struct blasst_packed_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  float* lse;
+  const int* cu_q;
+  const int* cu_k;
+  int n_seq, Tq, Tk, Hq, Hkv, d;
+  long long q_st, q_sh, k_st, k_sh, v_st, v_sh;
+  int causal;
+  float scale;
+  int dtype;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+} blasst_packed_args;
+BLASST_API int blasst_packed_fwd(const blasst_packed_args* args);
+
+/* Attention of new tokens (a chunk, or one per sequence) over the paged cache,
+ * exact. kv_lens[s] counts the cached tokens with the new ones (already
+ * written, e.g. by blasst_append); query token i of sequence s sees key j when
+ * j <= i + (kv_lens[s] - len_q) (causal = 1) or every cached key (causal = 0).
+ * A sequence without new tokens costs nothing.
+ *   page_size  a multiple of 8; other arguments as in blasst_packed_fwd. */
+typedef struct blasst_paged_args {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  void* o;
+  float* lse;
+  const int* page_table;
+  const int* kv_lens;
+  const int* cu_q;
+  int n_seq, Tq, Hq, Hkv, d;
+  int n_pages, page_size, table_width;
+  long long table_stride;
+  long long q_st, q_sh, kp_sp, kp_st, kp_sh, vp_sp, vp_st, vp_sh;
+  int causal;
+  float scale;
+  int dtype;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+} blasst_paged_args;
+BLASST_API int blasst_paged_fwd(const blasst_paged_args* args);
+
+/* Workspace bytes of blasst_packed_fwd and blasst_paged_fwd on the current
+ * device (0 if it cannot be queried): fp32 partial rows of the items that
+ * ranges of the shared list cut, two per SM. Host only. */
+BLASST_API size_t blasst_seq_workspace_bytes(int d);
 
 /* Synchronises `stream`, then returns (and clears) the device error word:
  * BLASST_OK, BLASST_ETIMEOUT if a kernel's bounded wait gave up, or
