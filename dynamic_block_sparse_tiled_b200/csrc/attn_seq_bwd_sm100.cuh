@@ -1,0 +1,757 @@
+// attn_seq_bwd_sm100.cuh - gradients of exact attention over packed sequences
+// on sm_100a (tcgen05 + TMEM + TMA).
+//
+//   P = exp(scale q.k - lse),  D_i = dO_i . o_i,  dS = P (dO.v - D),
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K,
+// dK and dV summed over the query heads of a KV head.
+//
+// Every output row is summed by one CTA in one order: no atomics, no 32-bit
+// dQ in memory, and the same bits from every run. The price is that P and dS
+// are formed twice, once for dK and dV and once for dQ (7 products of tile
+// size instead of 5); forming them once needs a 32-bit dQ that all key tiles
+// add into (cleared, added to in L2 through shared memory, converted), and
+// those bytes pass through the shared memory that feeds the tensor core.
+//
+// One CTA per item, one launch for both kinds:
+//   key item   128 keys of one sequence and KV head. K and V stay; tiles of 128
+//              rows (token, query head of the group) of Q and dO stream past:
+//                S^T = K Q^T, dP^T = V dO^T   (lanes = keys)
+//                dV += P^T dO, dK += dS^T Q   (A from TMEM)
+//   row item   128 rows of one sequence and KV head. Q and dO stay; tiles of
+//              128 keys of K and V stream past:
+//                S = Q K^T, dP = dO V^T       (lanes = rows)
+//                dQ += dS K                   (A from TMEM)
+// Warps 0-7 form P and dS (thread = TMEM lane, warpgroup w = columns
+// [64 w, 64 w + 64)); warp 8: TMA producer; warp 9: tcgen05 issuer; warp 10:
+// finds the item, then (key item) brings the rows' statistics. P and dS go
+// back to TMEM as 16-bit pairs, each warpgroup's over its own columns.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/blasst.h"
+#include "attn_seq_sm100.cuh"
+#include "ptx_sm100.cuh"
+
+namespace blasst {
+
+struct SeqBwdParams {
+  void* dq;  // [Tq, Hq, D]
+  void* dk;  // [Tk, Hkv, D]
+  void* dv;  // [Tk, Hkv, D]
+  const float2* stats;       // [Hkv][Tq][g]: (-lse log2 e + P's shift, D)
+  const uint32_t* norms;     // [Hkv][2]: largest |dO row|^2, |v row|^2 (bits); null: dS is not scaled
+  const int* cu_q;
+  const int* cu_k;
+  int n_seq, Tq, Tk, Hq, Hkv, g;
+  int rt;       // tokens per 128-row tile
+  int n_key, n_row;  // most items per KV head
+  int causal;
+  float scale, scale_log2;
+  float p_unscale;  // undoes P's shift
+  int* err;
+  uint64_t timeout_ns;
+};
+
+// fp16 only: P is kept as 2^8 P, so that the P of long rows (1 / keys) stay
+// normal numbers, and dS as 2^k dS with k from the largest rows of dO and v:
+// |dS| <= 2 |dO_i| |v_j|, so 2^k dS < 2^15 never overflows and uses the whole
+// range. Powers of two, undone in 32 bits at the end.
+template <typename T>
+constexpr float seq_bwd_p_shift() {
+  return SeqType<T>::kFormat == 0 ? 8.0f : 0.0f;
+}
+
+struct SeqBwdRowsParams {
+  const void* o;
+  const void* dout;
+  const void* v;
+  const float* lse;  // [Tq, Hq]
+  float2* stats;
+  uint32_t* norms;  // null: not needed
+  const int* cu_q;
+  const int* cu_k;
+  long long o_st, o_sh, do_st, do_sh, v_st, v_sh;
+  int n_seq, Tq, Tk, Hq, Hkv, g;
+  int row_blocks;  // blocks over the query rows; those behind them take v
+  float shift;
+};
+
+constexpr int kBwdRowsPerBlock = 64;
+
+// Row pass: D_i and the scaled lse of every row, laid out so that a tile's
+// rows are contiguous; with `norms` the largest rows of dO and v too. A warp
+// takes two rows at a time, 16 lanes each (8 values = 16 bytes per lane and step).
+template <int D, typename T>
+__global__ void __launch_bounds__(256) blasst_seq_bwd_rows_kernel(const SeqBwdRowsParams p) {
+  constexpr int LPR = D / 8;         // lanes per row
+  constexpr int RPW = 32 / LPR;      // rows per warp
+  const int hk = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane / LPR, at = lane % LPR;
+  float most = 0.0f;
+  const bool of_v = static_cast<int>(blockIdx.x) >= p.row_blocks;
+  const long long block = of_v ? blockIdx.x - p.row_blocks : blockIdx.x;
+  const long long all = static_cast<long long>(p.Tq) * p.g;
+  // what belongs to no sequence is not read (it may hold anything)
+  const int* cu = of_v ? p.cu_k : p.cu_q;
+  const int per = of_v ? 1 : p.g;
+  const long long begin = static_cast<long long>(max(cu[0], 0)) * per;
+  const long long end = static_cast<long long>(min(cu[p.n_seq], of_v ? p.Tk : p.Tq)) * per;
+#pragma unroll
+  for (int i = 0; i < kBwdRowsPerBlock / (8 * RPW); ++i) {
+    const long long r = block * kBwdRowsPerBlock + (i * 8 + warp) * RPW + sub;
+    float dot = 0.0f, sq = 0.0f;
+    const bool owned = r >= begin && r < end;
+    if (owned) {
+      const T* a;
+      const T* b;
+      if (of_v) {
+        a = b = static_cast<const T*>(p.v) + r * p.v_st + hk * p.v_sh + at * 8;
+      } else {
+        const long long t = r / p.g, h = hk * p.g + r % p.g;
+        a = static_cast<const T*>(p.dout) + t * p.do_st + h * p.do_sh + at * 8;
+        b = static_cast<const T*>(p.o) + t * p.o_st + h * p.o_sh + at * 8;
+      }
+      uint4 av = *reinterpret_cast<const uint4*>(a), bv = *reinterpret_cast<const uint4*>(b);
+      const T* ae = reinterpret_cast<const T*>(&av);
+      const T* be = reinterpret_cast<const T*>(&bv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = static_cast<float>(ae[j]);
+        dot = fmaf(x, static_cast<float>(be[j]), dot);
+        sq = fmaf(x, x, sq);
+      }
+    }
+#pragma unroll
+    for (int d = LPR / 2; d > 0; d >>= 1) {
+      dot += __shfl_xor_sync(0xffffffffu, dot, d);
+      sq += __shfl_xor_sync(0xffffffffu, sq, d);
+    }
+    if (owned && !of_v && at == 0) {
+      const long long t = r / p.g, h = hk * p.g + r % p.g;
+      const float l = p.lse[t * p.Hq + h];
+      p.stats[static_cast<long long>(hk) * all + r] =
+          make_float2(l == -INFINITY ? -INFINITY : fmaf(l, -1.4426950408889634f, p.shift), dot);
+    }
+    most = fmaxf(most, sq);
+  }
+  if (p.norms) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+    __shared__ float part[8];
+    if (lane == 0) part[warp] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < 8; ++i) most = fmaxf(most, part[i]);
+      // a maximum: the order of the blocks does not matter
+      if (most > 0.0f) atomicMax(p.norms + 2 * hk + (of_v ? 1 : 0), __float_as_uint(most));
+    }
+  }
+}
+
+template <int D>
+struct SeqBwdCfg {
+  static constexpr int NTHREADS = 384;
+  // registers per thread, as in the forward
+  static constexpr int REGS = 168, REGS_SOFT = 216, REGS_REST = 72;
+  static constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_ROWS = 10;
+  static constexpr int BK = 128;
+  static constexpr int DBOX = D / 64;
+  static constexpr int BOX = 128 * 128;
+  static constexpr int TILE = BOX * DBOX;
+  // ring of the streamed tile that is read twice (Q, K) and of the other (dO, V)
+  static constexpr int NS1 = D == 128 ? 3 : 4;
+  static constexpr int NS2 = D == 128 ? 2 : 3;
+  static constexpr int NST = 2;  // slots of row statistics
+  static constexpr int OFF_A = 0;  // what stays: K, V or Q, dO
+  static constexpr int OFF_R1 = 2 * TILE;
+  static constexpr int OFF_R2 = OFF_R1 + NS1 * TILE;
+  static constexpr int OFF_ST = OFF_R2 + NS2 * TILE;  // [NST][2][128] fp32
+  static constexpr int OFF_BAR = OFF_ST + NST * 1024;
+  static constexpr int B_A = 0;
+  static constexpr int B_TAIL = 1;
+  static constexpr int B_F1 = 2;
+  static constexpr int B_E1 = B_F1 + NS1;
+  static constexpr int B_F2 = B_E1 + NS1;
+  static constexpr int B_E2 = B_F2 + NS2;
+  static constexpr int B_S = B_E2 + NS2;   // S written
+  static constexpr int B_P = B_S + 1;      // key item: P written; row item: S read (8 warps)
+  static constexpr int B_DP = B_P + 1;     // [2] dP written
+  static constexpr int B_DS = B_DP + 2;    // [2] dS written (8 warps)
+  static constexpr int B_STF = B_DS + 2;   // [NST] statistics there
+  static constexpr int B_STE = B_STF + NST;  // [NST] read (8 warps)
+  static constexpr int B_ACC = B_STE + NST;
+  static constexpr int B_DRAIN = B_ACC + 1;
+  static constexpr int NBAR = B_DRAIN + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  // misc words: [0] tmem base, [1] abort, [3] always 0, [4..] the item
+  static constexpr int OFF_ITEM = OFF_MISC + 16;
+  static constexpr int SMEM_BYTES = OFF_ITEM + 48;
+  static constexpr int S_COL = 0;
+  // key item: dP, dV, dK behind S; row item: dQ, then two dP
+  static constexpr int K_DP = 128, K_DV = 256, K_DK = 384;
+  static constexpr int R_DQ = 128, R_DP = 256;
+  static constexpr int TMEM_COLS = 512;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+};
+
+// The CTA's item. Tokens and keys count from the sequence's first.
+struct SeqBwdItem {
+  int kind;      // 0 none, 1 key item, 2 row item
+  int hk, q0, qlen, k0, kvlen, off;
+  int at;        // first key, or first token
+  int first;     // key item: first token that is streamed
+  int steps;     // streamed tiles
+};
+
+template <int D, typename T>
+__global__ void __launch_bounds__(384, 1)
+    blasst_seq_bwd_kernel(const __grid_constant__ CUtensorMap tmQ,
+                          const __grid_constant__ CUtensorMap tmDO,
+                          const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const SeqBwdParams p) {
+  using C = SeqBwdCfg<D>;
+  constexpr uint32_t IDESC_S = ptx::idesc_f32acc(SeqType<T>::kFormat, 128, 128, false);
+  constexpr uint32_t IDESC_G = ptx::idesc_f32acc(SeqType<T>::kFormat, 128, D, true);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw;
+  const uint32_t sb = ptx::smem_u32(smem);
+  volatile int* misc = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = misc + 1;
+  volatile int* itemw = reinterpret_cast<volatile int*>(smem + C::OFF_ITEM);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
+  if ((sb & 1023u) != 0u) {  // uniform; the tiles need 1 KB alignment
+    if (threadIdx.x == 0) seq_record_error(p.err, BLASST_EUNSUPPORTED);
+    return;
+  }
+
+  // ---- the item: key items of all heads first, then row items -------------
+  if (warp == C::WARP_ROWS) {
+    const int n_keys = p.n_key * p.Hkv;
+    const bool key = static_cast<int>(blockIdx.x) < n_keys;
+    const int idx = key ? blockIdx.x : blockIdx.x - n_keys;
+    const int per = key ? p.n_key : p.n_row;
+    const int h = idx / per, want = idx % per;
+    // after a wait gave up, calls before blasst_check do nothing
+    const bool live = !(p.err && *reinterpret_cast<volatile int*>(p.err) == BLASST_ETIMEOUT);
+    auto span = [&](int s) -> SeqSpan {
+      return seq_span(p.cu_q, p.cu_k, nullptr, 0, p.Tq, p.Tk, p.rt, s, p.err);
+    };
+    SeqBwdItem it{};
+    int before = 0;
+    // longest first under a causal mask: the first keys, the last rows
+    for (int s0 = 0; s0 < p.n_seq && it.kind == 0 && live; s0 += 32) {
+      const int i = s0 + lane;
+      const int s = key ? i : p.n_seq - 1 - i;
+      int tiles = 0;
+      if (i < p.n_seq) {
+        const SeqSpan q = span(s);
+        tiles = key ? (q.kvlen + C::BK - 1) / C::BK : q.tiles;
+      }
+      int upto = tiles;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += v;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, want < before + upto);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        const int n = __shfl_sync(0xffffffffu, tiles, l);
+        const int start = before + __shfl_sync(0xffffffffu, upto, l) - n;
+        const int i_hit = s0 + l;
+        const SeqSpan q = span(key ? i_hit : p.n_seq - 1 - i_hit);
+        it.hk = h;
+        it.q0 = q.q0;
+        it.qlen = q.qlen;
+        it.k0 = q.k0;
+        it.kvlen = q.kvlen;
+        it.off = q.off;
+        if (key) {
+          it.kind = 1;
+          it.at = (want - start) * C::BK;
+          // from the first token that sees a key of the tile: no row without
+          // keys is ever streamed
+          it.first = p.causal ? min(max(it.at - q.off, 0), q.qlen) : 0;
+          it.steps = (q.qlen - it.first + p.rt - 1) / p.rt;
+        } else {
+          it.kind = 2;
+          it.at = (n - 1 - (want - start)) * p.rt;
+          const int last = min(it.at + p.rt, q.qlen) - 1;
+          const int keys = p.causal ? min(max(q.off + last + 1, 0), q.kvlen) : q.kvlen;
+          it.steps = (keys + C::BK - 1) / C::BK;
+        }
+      }
+      before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) {
+      itemw[0] = it.kind;
+      itemw[1] = it.hk;
+      itemw[2] = it.q0;
+      itemw[3] = it.qlen;
+      itemw[4] = it.k0;
+      itemw[5] = it.kvlen;
+      itemw[6] = it.off;
+      itemw[7] = it.at;
+      itemw[8] = it.first;
+      itemw[9] = it.steps;
+    }
+  }
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(bar(C::B_A), 1);
+    ptx::mbar_init(bar(C::B_TAIL), 1);
+    for (int i = 0; i < C::NS1; ++i) {
+      ptx::mbar_init(bar(C::B_F1 + i), 1);
+      ptx::mbar_init(bar(C::B_E1 + i), 1);
+    }
+    for (int i = 0; i < C::NS2; ++i) {
+      ptx::mbar_init(bar(C::B_F2 + i), 1);
+      ptx::mbar_init(bar(C::B_E2 + i), 1);
+    }
+    ptx::mbar_init(bar(C::B_S), 1);
+    ptx::mbar_init(bar(C::B_P), 8);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar(C::B_DP + i), 1);
+      ptx::mbar_init(bar(C::B_DS + i), 8);
+    }
+    for (int i = 0; i < C::NST; ++i) {
+      ptx::mbar_init(bar(C::B_STF + i), 1);
+      ptx::mbar_init(bar(C::B_STE + i), 8);
+    }
+    ptx::mbar_init(bar(C::B_ACC), 1);
+    ptx::mbar_init(bar(C::B_DRAIN), 1);
+    for (int i = 1; i < 4; ++i) misc[i] = 0;
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  SeqBwdItem it;
+  it.kind = itemw[0];
+  if (it.kind == 0) return;  // uniform, nothing in flight
+  it.hk = itemw[1];
+  it.q0 = itemw[2];
+  it.qlen = itemw[3];
+  it.k0 = itemw[4];
+  it.kvlen = itemw[5];
+  it.off = itemw[6];
+  it.at = itemw[7];
+  it.first = itemw[8];
+  it.steps = itemw[9];
+  const bool key = it.kind == 1;
+  const int n = it.steps;
+  const int box_rows = p.g * p.rt;
+  if (warp == C::WARP_MMA) {
+    ptx::tmem_alloc(ptx::smem_u32(const_cast<int*>(misc)), C::TMEM_COLS);
+    ptx::tmem_relinquish();
+  }
+  if (key && box_rows < 128) {
+    // rows of a streamed tile that no copy writes: contracted over, so 0
+    for (int s = 0; s < C::NS1 + C::NS2; ++s)
+      for (int x = 0; x < C::DBOX; ++x)
+        for (int i = box_rows * 8 + threadIdx.x; i < 128 * 8; i += C::NTHREADS)
+          *reinterpret_cast<uint4*>(smem + C::OFF_R1 + s * C::TILE + x * C::BOX + i * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+    ptx::fence_proxy_async_smem();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+  auto fail = [&]() {
+    *abort_flag = 1;
+    seq_record_error(p.err, BLASST_ETIMEOUT);
+  };
+  auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
+    bool r = true;
+    if (lane == 0) r = ptx::mbar_wait(b, parity, abort_flag, p.timeout_ns);
+    return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
+  };
+  // dS = (2^shift P) (c dP - c D) = 2^k P (dP - D)
+  float c = 1.0f, ds_unscale = 1.0f;
+  if (p.norms && n > 0) {
+    const float nm = sqrtf(__uint_as_float(p.norms[2 * it.hk])) *
+                     sqrtf(__uint_as_float(p.norms[2 * it.hk + 1]));
+    const int k = nm > 0.0f && nm < INFINITY ? 14 - (ilogbf(nm) + 1) : 0;
+    c = p.p_unscale * exp2f(static_cast<float>(k));
+    ds_unscale = exp2f(static_cast<float>(-k));
+  }
+
+  if (warp >= 8) {
+    ptx::reg_give<C::REGS_REST>();
+    if (warp == C::WARP_LOAD) {
+      // ======================= TMA producer ==================================
+      // rows (key item: tokens; row item: keys) of a streamed tile, and the
+      // rows of each that count
+      const CUtensorMap* a1 = key ? &tmK : &tmQ;
+      const CUtensorMap* a2 = key ? &tmV : &tmDO;
+      const CUtensorMap* s1 = key ? &tmQ : &tmK;
+      const CUtensorMap* s2 = key ? &tmDO : &tmV;
+      const int a_rows = key ? C::BK : box_rows, s_rows = key ? box_rows : C::BK;
+      auto load = [&](const CUtensorMap* tm, bool of_keys, uint32_t dst, int row, uint32_t b) {
+#pragma unroll
+        for (int x = 0; x < C::DBOX; ++x) {
+          if (of_keys) ptx::tma_load_4d(dst + x * C::BOX, tm, x * 64, it.k0 + row, it.hk, 0, b);
+          else ptx::tma_load_4d(dst + x * C::BOX, tm, x * 64, 0, it.q0 + row, it.hk, b);
+        }
+      };
+      bool ok = true;
+      bool a_sent = false;
+      uint32_t tails = 0, in1 = 0, in2 = 0;  // loads whose full barrier the copy itself completes
+      bool tail_open = false;
+      for (int i = 0; i < n && ok; ++i) {
+        const int row = key ? it.first + i * p.rt : i * C::BK;
+        const int valid = key ? min(p.rt, it.qlen - row) * p.g : min(C::BK, it.kvlen - row);
+        const bool tail = valid < s_rows;
+#pragma unroll 1
+        for (int w = 0; w < 2 && ok; ++w) {
+          const uint32_t slots = w ? C::NS2 : C::NS1;
+          const uint32_t slot = static_cast<uint32_t>(i) % slots, turn = static_cast<uint32_t>(i) / slots;
+          const uint32_t full = bar((w ? C::B_F2 : C::B_F1) + slot);
+          const int off = (w ? C::OFF_R2 : C::OFF_R1) + static_cast<int>(slot) * C::TILE;
+          // rows behind the sequence's end may hold anything, and 0 x NaN is
+          // NaN: what is contracted over is cleared (V is not, its products
+          // are replaced)
+          const bool clear = tail && (key || w == 0);
+          const uint32_t fb = clear ? bar(C::B_TAIL) : full;
+          if (lane == 0) {
+            if (turn > 0)
+              ok = ptx::mbar_wait(bar((w ? C::B_E2 : C::B_E1) + slot), (turn - 1) & 1, abort_flag,
+                                  p.timeout_ns);
+            if (ok) {
+              if (i == 0 && w == 0) {
+                ptx::mbar_arrive_expect_tx(bar(C::B_A), 2 * C::DBOX * a_rows * 128);
+                load(a1, key, sb + C::OFF_A, it.at, bar(C::B_A));
+              }
+              ptx::mbar_arrive_expect_tx(fb, C::DBOX * s_rows * 128);
+              load(w ? s2 : s1, !key, sb + off, row, fb);
+              if (i == 0 && w == 0) load(a2, key, sb + C::OFF_A + C::TILE, it.at, bar(C::B_A));
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          a_sent = true;
+          if (w) in2 = i + 1;
+          else in1 = i + 1;
+          if (clear) {
+            tail_open = true;
+            ok = warp_wait(bar(C::B_TAIL), tails & 1);
+            if (!ok) break;
+            ++tails;
+            tail_open = false;
+            for (int u = valid * 8 + lane; u < 128 * 8; u += 32)
+#pragma unroll
+              for (int x = 0; x < C::DBOX; ++x)
+                *reinterpret_cast<uint4*>(smem + off + x * C::BOX + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(full);
+          }
+        }
+      }
+      if (!ok && lane == 0) {
+        fail();
+        // copies in flight land before the CTA exits (1 ms each is ample)
+        const uint64_t drain_ns = p.timeout_ns < 1000000ull ? p.timeout_ns : 1000000ull;
+        if (a_sent) ptx::mbar_wait(bar(C::B_A), 0, &misc[3], drain_ns);
+        if (tail_open) ptx::mbar_wait(bar(C::B_TAIL), tails & 1, &misc[3], drain_ns);
+        for (uint32_t k = in1 < C::NS1 ? 0 : in1 - C::NS1; k < in1; ++k)
+          ptx::mbar_wait(bar(C::B_F1 + k % C::NS1), (k / C::NS1) & 1, &misc[3], drain_ns);
+        for (uint32_t k = in2 < C::NS2 ? 0 : in2 - C::NS2; k < in2; ++k)
+          ptx::mbar_wait(bar(C::B_F2 + k % C::NS2), (k / C::NS2) & 1, &misc[3], drain_ns);
+      }
+    } else if (warp == C::WARP_MMA) {
+      // ======================= tcgen05 issuer ================================
+      if (lane == 0 && n > 0) {
+        const uint64_t a_desc = ptx::sw128_desc(sb + C::OFF_A, 16, 1024);
+        const uint64_t b1_desc = ptx::sw128_desc(sb + C::OFF_R1, 16, 1024);
+        const uint64_t b2_desc = ptx::sw128_desc(sb + C::OFF_R2, 16, 1024);
+        const uint64_t g1_desc = ptx::sw128_desc(sb + C::OFF_R1, C::BOX, 1024);
+        const uint64_t g2_desc = ptx::sw128_desc(sb + C::OFF_R2, C::BOX, 1024);
+        constexpr uint64_t TS = C::TILE >> 4;
+        auto wait = [&](int b, uint32_t parity) -> bool {
+          return ptx::mbar_wait(bar(b), parity, abort_flag, p.timeout_ns);
+        };
+        // 128 x 128 products of what stays and a streamed tile (K-major both)
+        auto score = [&](uint32_t d_tm, uint64_t a, uint64_t b) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t o = static_cast<uint64_t>(((kk >> 2) * C::BOX + (kk & 3) * 32) >> 4);
+            ptx::mma_ss(d_tm, a + o, b + o, IDESC_S, kk > 0 ? 1u : 0u);
+          }
+        };
+        // 128 x D: 16-bit pairs in TMEM (each warpgroup's over its columns)
+        // times a streamed tile
+        auto grad = [&](uint32_t d_tm, uint32_t a_tm, uint64_t b, bool add) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            ptx::mma_ts(d_tm, a_tm + (kk >> 2) * 64 + (kk & 3) * 8,
+                        b + static_cast<uint64_t>(kk * (2048 >> 4)), IDESC_G,
+                        add || kk > 0 ? 1u : 0u);
+        };
+        auto issue_s = [&](int i) -> bool {
+          const uint32_t slot = static_cast<uint32_t>(i) % C::NS1, turn = static_cast<uint32_t>(i) / C::NS1;
+          if (!wait(C::B_F1 + slot, turn & 1)) return false;
+          ptx::tc_fence_after();
+          score(tmem + C::S_COL, a_desc, b1_desc + slot * TS);
+          ptx::mma_commit(bar(C::B_S));
+          return true;
+        };
+        auto issue_dp = [&](int i) -> bool {
+          const uint32_t slot = static_cast<uint32_t>(i) % C::NS2, turn = static_cast<uint32_t>(i) / C::NS2;
+          if (!wait(C::B_F2 + slot, turn & 1)) return false;
+          ptx::tc_fence_after();
+          score(tmem + (key ? C::K_DP : C::R_DP + (i & 1) * 128), a_desc + TS, b2_desc + slot * TS);
+          ptx::mma_commit(bar(C::B_DP + (i & 1)));
+          if (!key) ptx::mma_commit(bar(C::B_E2 + slot));
+          return true;
+        };
+        bool ok = wait(C::B_A, 0);
+        ok = ok && issue_s(0) && issue_dp(0);
+        for (int i = 0; i < n && ok; ++i) {
+          const uint32_t s1 = static_cast<uint32_t>(i) % C::NS1, s2 = static_cast<uint32_t>(i) % C::NS2;
+          if (key) {
+            // dV(i), S(i+1), dK(i), dP(i+1): while dS(i) is formed the tensor
+            // core does the first two, while P(i+1) is formed the others
+            ok = wait(C::B_P, i & 1);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            grad(tmem + C::K_DV, tmem + C::S_COL, g2_desc + s2 * TS, i > 0);
+            ptx::mma_commit(bar(C::B_E2 + s2));
+            if (i + 1 < n) ok = issue_s(i + 1);  // over P(i), which dV(i) has read by then
+            ok = ok && wait(C::B_DS + (i & 1), (i >> 1) & 1);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            grad(tmem + C::K_DK, tmem + C::K_DP, g1_desc + s1 * TS, i > 0);
+            ptx::mma_commit(bar(C::B_E1 + s1));
+            if (i + 1 < n) ok = issue_dp(i + 1);
+          } else {
+            if (i + 1 < n) {
+              ok = wait(C::B_P, i & 1);
+              ok = ok && issue_s(i + 1) && issue_dp(i + 1);
+            }
+            ok = ok && wait(C::B_DS + (i & 1), (i >> 1) & 1);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            grad(tmem + C::R_DQ, tmem + C::R_DP + (i & 1) * 128, g1_desc + s1 * TS, i > 0);
+            ptx::mma_commit(bar(C::B_E1 + s1));
+          }
+        }
+        ptx::mma_commit(bar(C::B_ACC));
+        if (!ok) fail();
+        // every product has completed before TMEM is freed
+        ptx::mma_commit(bar(C::B_DRAIN));
+        ptx::mbar_wait(bar(C::B_DRAIN), 0, &misc[3], p.timeout_ns);
+      }
+    } else if (warp == C::WARP_ROWS && key) {
+      // ======================= statistics of the streamed rows ===============
+      const float2* base = p.stats + (static_cast<long long>(it.hk) * p.Tq + it.q0) * p.g;
+      bool ok = true;
+      for (int i = 0; i < n && ok; ++i) {
+        const int slot = i % C::NST;
+        const int tok = it.first + i * p.rt;
+        const int valid = min(p.rt, it.qlen - tok) * p.g;
+        float2 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = lane + 32 * u;
+          v[u] = r < valid ? base[static_cast<long long>(tok) * p.g + r] : make_float2(-INFINITY, 0.0f);
+        }
+        if (i >= C::NST) ok = warp_wait(bar(C::B_STE + slot), (i / C::NST - 1) & 1);
+        if (!ok) break;
+        float* st = reinterpret_cast<float*>(smem + C::OFF_ST + slot * 1024);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          st[lane + 32 * u] = v[u].x;
+          st[128 + lane + 32 * u] = -v[u].y * c;
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_STF + slot));
+      }
+      if (!ok && lane == 0) fail();
+    }
+  } else {
+    ptx::reg_take<C::REGS_SOFT>();
+    // ======================= P and dS ========================================
+    const int wg = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;  // TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + lane_base + C::S_COL + wg * 64;
+    const float sl2 = p.scale_log2;
+    bool ok = true;
+    // row item: the lane's token and statistics
+    const int tok = it.at + row / p.g;
+    const bool exists = key ? it.at + row < it.kvlen : row < box_rows && tok < it.qlen;
+    float nl2 = -INFINITY, dcol = 0.0f;
+    int limit = 0, least = 0;
+    if (!key) {
+      if (exists) {
+        const float2 v = p.stats[(static_cast<long long>(it.hk) * p.Tq + it.q0 + it.at) * p.g + row];
+        nl2 = v.x;
+        dcol = -v.y * c;
+      }
+      limit = p.causal ? min(it.off + tok + 1, it.kvlen) : it.kvlen;
+      least = p.causal ? min(it.off + it.at + 1, it.kvlen) : it.kvlen;
+    }
+    float pv[64];
+    // the lane's visible columns of tile i: [lo, hi), relative to the warpgroup's
+    auto columns = [&](int i, int& lo, int& hi) -> bool {
+      lo = 0;
+      hi = 64;
+      if (key) {
+        if (!p.causal) return false;
+        const int first = it.first + i * p.rt + it.off;  // key the tile's first token sees last
+        lo = max(it.at + row - first, 0) * p.g - wg * 64;
+        return it.at + C::BK - 1 > first;
+      }
+      const int col0 = i * C::BK;
+      hi = limit - col0 - wg * 64;
+      return col0 + C::BK > least;
+    };
+    auto form_p = [&](int i) -> bool {
+      if (!warp_wait(bar(C::B_S), i & 1)) return false;
+      if (key && !warp_wait(bar(C::B_STF + i % C::NST), (i / C::NST) & 1)) return false;
+      ptx::tc_fence_after();
+      uint32_t sv[64];
+      ptx::tmem_ld32p(s_tm, sv);
+      ptx::tmem_ld32p(s_tm + 32, sv + 32);
+      ptx::tmem_wait_ld();
+      if (!key) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_P));
+      }
+      const float4* st = reinterpret_cast<const float4*>(smem + C::OFF_ST + (i % C::NST) * 1024) + wg * 16;
+#pragma unroll
+      for (int j = 0; j < 64; j += 4) {
+        float4 a = make_float4(nl2, nl2, nl2, nl2);
+        if (key) a = st[j / 4];
+        float x0, x1, x2, x3;
+        ptx::fma2(x0, x1, __uint_as_float(sv[j]), __uint_as_float(sv[j + 1]), sl2, sl2, a.x, a.y);
+        ptx::fma2(x2, x3, __uint_as_float(sv[j + 2]), __uint_as_float(sv[j + 3]), sl2, sl2, a.z, a.w);
+        pv[j] = ptx::ex2(x0);
+        pv[j + 1] = ptx::ex2(x1);
+        pv[j + 2] = ptx::ex2(x2);
+        pv[j + 3] = ptx::ex2(x3);
+      }
+      int lo, hi;
+      if (columns(i, lo, hi)) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+          if (j < lo || j >= hi) pv[j] = 0.0f;
+      }
+      if (key) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) pk[j] = seq_pack2<T>(pv[2 * j], pv[2 * j + 1]);
+        ptx::tmem_st32(s_tm, pk);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_P));
+      }
+      return true;
+    };
+    auto form_ds = [&](int i) -> bool {
+      if (!warp_wait(bar(C::B_DP + (i & 1)), (i >> 1) & 1)) return false;
+      ptx::tc_fence_after();
+      const uint32_t dp_tm =
+          tmem + lane_base + (key ? C::K_DP : C::R_DP + (i & 1) * 128) + wg * 64;
+      uint32_t dp[64];
+      ptx::tmem_ld32p(dp_tm, dp);
+      ptx::tmem_ld32p(dp_tm + 32, dp + 32);
+      ptx::tmem_wait_ld();
+      const float4* st =
+          reinterpret_cast<const float4*>(smem + C::OFF_ST + (i % C::NST) * 1024 + 512) + wg * 16;
+      int lo, hi;
+      const bool cut = columns(i, lo, hi);
+      uint32_t pk[32];
+#pragma unroll
+      for (int j = 0; j < 64; j += 4) {
+        float4 a = make_float4(dcol, dcol, dcol, dcol);
+        if (key) a = st[j / 4];
+        float x[4];
+        ptx::fma2(x[0], x[1], __uint_as_float(dp[j]), __uint_as_float(dp[j + 1]), c, c, a.x, a.y);
+        ptx::fma2(x[2], x[3], __uint_as_float(dp[j + 2]), __uint_as_float(dp[j + 3]), c, c, a.z, a.w);
+        ptx::mul2(x[0], x[1], x[0], x[1], pv[j], pv[j + 1]);
+        ptx::mul2(x[2], x[3], x[2], x[3], pv[j + 2], pv[j + 3]);
+        if (cut) {  // a masked place may hold anything: 0, whatever dP is
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (j + u < lo || j + u >= hi) x[u] = 0.0f;
+        }
+        pk[j / 2] = seq_pack2<T>(x[0], x[1]);
+        pk[j / 2 + 1] = seq_pack2<T>(x[2], x[3]);
+      }
+      ptx::tmem_st32(dp_tm, pk);
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(bar(C::B_DS + (i & 1)));
+        if (key) ptx::mbar_arrive(bar(C::B_STE + i % C::NST));
+      }
+      return true;
+    };
+    if (n > 0) ok = form_p(0);
+    for (int i = 0; i < n && ok; ++i) {
+      ok = form_ds(i);
+      if (ok && i + 1 < n) ok = form_p(i + 1);
+    }
+    if (ok && n > 0) ok = warp_wait(bar(C::B_ACC), 0);
+    ok = ok && *abort_flag == 0;
+    ok = __all_sync(0xffffffffu, ok) != 0;
+    if (!ok) {
+      fail();
+    } else {
+      ptx::tc_fence_after();
+      // key item: warpgroup 0 writes dV, 1 writes dK; row item: half of the
+      // columns of dQ each
+      const int chunks = key ? D / 32 : D / 64;
+      const int c0 = key ? 0 : wg * (D / 64);
+      const uint32_t acc = tmem + lane_base + (key ? (wg ? C::K_DK : C::K_DV) : C::R_DQ);
+      const float f = key && wg == 0 ? p.p_unscale : p.scale * ds_unscale;
+      T* out;
+      if (key) out = static_cast<T*>(wg ? p.dk : p.dv) +
+                     (static_cast<long long>(it.k0 + it.at + row) * p.Hkv + it.hk) * D;
+      else out = static_cast<T*>(p.dq) +
+                 (static_cast<long long>(it.q0 + tok) * p.Hq + it.hk * p.g + row % p.g) * D;
+#pragma unroll 1
+      for (int k = c0; k < c0 + chunks; ++k) {
+        uint32_t r[32];
+        if (n > 0) {
+          ptx::tmem_ld32(acc + 32 * k, r);
+          ptx::tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = 0u;
+        }
+        if (exists) {
+          uint4* dst = reinterpret_cast<uint4*>(out + 32 * k);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              w[u] = seq_pack2<T>(__uint_as_float(r[8 * j + 2 * u]) * f,
+                                  __uint_as_float(r[8 * j + 2 * u + 1]) * f);
+            dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == C::WARP_MMA) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+}  // namespace blasst

@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "../../include/blasst.h"
+#include "attn_seq_bwd_sm100.cuh"
 #include "attn_seq_sm100.cuh"
 #include "capi_internal.h"
 #include "rotary_sm100.cuh"
@@ -132,6 +133,39 @@ int check_heads(int n_seq, int Tq, int Hq, int Hkv, int d, int dtype) {
   if (Hq / Hkv > 128) return BLASST_EUNSUPPORTED;
   if (dtype != BLASST_BF16 && dtype != BLASST_FP16) return BLASST_EUNSUPPORTED;
   return BLASST_OK;
+}
+
+constexpr size_t kNormBytes = 16;  // per KV head, two used words
+
+size_t bwd_workspace(int Tq, int Hq, int Hkv) {
+  return static_cast<size_t>(Hkv) * kNormBytes + static_cast<size_t>(Tq) * Hq * sizeof(float2);
+}
+
+template <int D, typename T>
+int launch_seq_bwd(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap& mk,
+                   const CUtensorMap& mv, const blasst::SeqBwdParams& p,
+                   const blasst::SeqBwdRowsParams& r, cudaStream_t stream) {
+  using C = blasst::SeqBwdCfg<D>;
+  auto kernel = blasst::blasst_seq_bwd_kernel<D, T>;
+  static int regs = 0;  // of this instantiation
+  if (const int rc = check_regs(kernel, C::REGS, regs)) return rc;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return cuda_status(e);
+  if (r.Tq > 0) {
+    if (r.norms) {
+      e = cudaMemsetAsync(r.norms, 0, static_cast<size_t>(r.Hkv) * 8, stream);
+      if (e != cudaSuccess) return cuda_status(e);
+    }
+    const int v_blocks = r.norms ? (r.Tk + blasst::kBwdRowsPerBlock - 1) / blasst::kBwdRowsPerBlock : 0;
+    blasst::blasst_seq_bwd_rows_kernel<D, T>
+        <<<dim3(static_cast<unsigned>(r.row_blocks + v_blocks), r.Hkv), 256, 0, stream>>>(r);
+    const int rc = cuda_status(cudaGetLastError());
+    if (rc != BLASST_OK) return rc;
+  }
+  const unsigned grid = static_cast<unsigned>(p.n_key + p.n_row) * p.Hkv;
+  kernel<<<grid, C::NTHREADS, C::SMEM_BYTES, stream>>>(mq, mdo, mk, mv, p);
+  return cuda_status(cudaGetLastError());
 }
 
 int elem_bytes(int dtype) { return dtype == BLASST_FP32 ? 4 : 2; }
@@ -367,6 +401,102 @@ int blasst_packed_fwd(const blasst_packed_args* a) {
     return BLASST_ECUDA;
   return run_seq(p, a->q, a->q_st, a->q_sh, a->d, a->scale, a->dtype, mk, mv, a->workspace, sms,
                  a->stream);
+}
+
+size_t blasst_packed_bwd_workspace_bytes(int Tq, int Hq, int Hkv) {
+  if (Tq < 0 || Hq <= 0 || Hkv <= 0) return 0;
+  return bwd_workspace(Tq, Hq, Hkv);
+}
+
+int blasst_packed_bwd(const blasst_packed_bwd_args* a) {
+  if (!a || !a->q || !a->k || !a->v || !a->o || !a->dout || !a->lse || !a->dq || !a->dk || !a->dv ||
+      !a->cu_q || !a->cu_k)
+    return BLASST_EINVAL;
+  for (const void* ptr : {a->q, a->k, a->v, a->o, a->dout, static_cast<const void*>(a->lse),
+                          static_cast<const void*>(a->dq), static_cast<const void*>(a->dk),
+                          static_cast<const void*>(a->dv)})
+    if (!aligned(ptr, 16)) return BLASST_EINVAL;
+  if (!aligned(a->cu_q, 4) || !aligned(a->cu_k, 4)) return BLASST_EINVAL;
+  if (const int rc = check_heads(a->n_seq, a->Tq, a->Hq, a->Hkv, a->d, a->dtype)) return rc;
+  if (a->Tk < 0 || std::isnan(a->scale)) return BLASST_EINVAL;
+  for (long long st : {a->q_st, a->q_sh, a->k_st, a->k_sh, a->v_st, a->v_sh, a->o_st, a->o_sh,
+                       a->do_st, a->do_sh})
+    if (!map_stride(st)) return BLASST_EINVAL;
+  if (!aligned(a->workspace, 16) || !a->workspace ||
+      a->workspace_bytes < bwd_workspace(a->Tq, a->Hq, a->Hkv))
+    return BLASST_EWORKSPACE;
+  if (a->n_seq == 0 || (a->Tq == 0 && a->Tk == 0)) return BLASST_OK;
+  blasst::SeqBwdParams p{};
+  p.g = a->Hq / a->Hkv;
+  p.rt = 128 / p.g;
+  // most tiles a KV head can have, whatever the lengths
+  const long long n_key = std::min<long long>(a->Tk, a->Tk / 128 + static_cast<long long>(a->n_seq));
+  const long long n_row = std::min<long long>(a->Tq, a->Tq / p.rt + static_cast<long long>(a->n_seq));
+  if ((n_key + n_row) * a->Hkv > 0x7fffffffll) return BLASST_EINVAL;
+  p.n_key = static_cast<int>(n_key);
+  p.n_row = static_cast<int>(n_row);
+  p.err = error_word();
+  if (!p.err) return BLASST_ECUDA;
+  const bool f16 = a->dtype == BLASST_FP16;
+  uint32_t* norms = static_cast<uint32_t*>(a->workspace);
+  float2* stats = reinterpret_cast<float2*>(static_cast<char*>(a->workspace) + a->Hkv * kNormBytes);
+  p.dq = a->dq;
+  p.dk = a->dk;
+  p.dv = a->dv;
+  p.stats = stats;
+  p.norms = f16 ? norms : nullptr;
+  p.cu_q = a->cu_q;
+  p.cu_k = a->cu_k;
+  p.n_seq = a->n_seq;
+  p.Tq = a->Tq;
+  p.Tk = a->Tk;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.causal = a->causal ? 1 : 0;
+  const double sc = a->scale > 0.0f ? static_cast<double>(a->scale) : 1.0 / std::sqrt(static_cast<double>(a->d));
+  p.scale = static_cast<float>(sc);
+  p.scale_log2 = static_cast<float>(sc * 1.4426950408889634);
+  const float shift = f16 ? blasst::seq_bwd_p_shift<__half>() : blasst::seq_bwd_p_shift<__nv_bfloat16>();
+  p.p_unscale = std::exp2(-shift);
+  p.timeout_ns = kTimeoutNs;
+  blasst::SeqBwdRowsParams r{};
+  r.o = a->o;
+  r.dout = a->dout;
+  r.v = a->v;
+  r.lse = a->lse;
+  r.stats = stats;
+  r.norms = f16 ? norms : nullptr;
+  r.cu_q = a->cu_q;
+  r.cu_k = a->cu_k;
+  r.o_st = a->o_st;
+  r.o_sh = a->o_sh;
+  r.do_st = a->do_st;
+  r.do_sh = a->do_sh;
+  r.v_st = a->v_st;
+  r.v_sh = a->v_sh;
+  r.n_seq = a->n_seq;
+  r.Tq = a->Tq;
+  r.Tk = a->Tk;
+  r.Hq = a->Hq;
+  r.Hkv = a->Hkv;
+  r.g = p.g;
+  r.row_blocks = static_cast<int>((static_cast<long long>(a->Tq) * p.g + blasst::kBwdRowsPerBlock - 1) /
+                                  blasst::kBwdRowsPerBlock);
+  r.shift = shift;
+  CUtensorMap mq, mdo, mk, mv;
+  if (!make_map4(&mq, a->q, a->dtype, {a->d, p.g, a->Tq, a->Hkv}, {a->q_sh, a->q_st, a->q_sh * p.g},
+                 p.g, p.rt) ||
+      !make_map4(&mdo, a->dout, a->dtype, {a->d, p.g, a->Tq, a->Hkv},
+                 {a->do_sh, a->do_st, a->do_sh * p.g}, p.g, p.rt) ||
+      !make_map4(&mk, a->k, a->dtype, {a->d, a->Tk, a->Hkv, 1}, {a->k_st, a->k_sh, 8}, 128, 1) ||
+      !make_map4(&mv, a->v, a->dtype, {a->d, a->Tk, a->Hkv, 1}, {a->v_st, a->v_sh, 8}, 128, 1))
+    return BLASST_ECUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(a->stream);
+  if (!f16)
+    return a->d == 128 ? launch_seq_bwd<128, __nv_bfloat16>(mq, mdo, mk, mv, p, r, s)
+                       : launch_seq_bwd<64, __nv_bfloat16>(mq, mdo, mk, mv, p, r, s);
+  return a->d == 128 ? launch_seq_bwd<128, __half>(mq, mdo, mk, mv, p, r, s)
+                     : launch_seq_bwd<64, __half>(mq, mdo, mk, mv, p, r, s);
 }
 
 int blasst_paged_fwd(const blasst_paged_args* a) {

@@ -16,7 +16,8 @@ import math
 
 __all__ = [
     "rope_frequencies", "rotary", "rotary_backward", "paged_append", "attention_packed",
-    "attention_paged", "blasst_seq_workspace_bytes",
+    "attention_packed_backward", "attention_paged", "blasst_seq_workspace_bytes",
+    "blasst_packed_bwd_workspace_bytes",
 ]
 
 _VP, _I, _LL, _F, _SZ = C.c_void_p, C.c_int, C.c_longlong, C.c_float, C.c_size_t
@@ -48,6 +49,16 @@ class PackedArgs(C.Structure):
                  ("workspace_bytes", _SZ), ("stream", _VP)])
 
 
+class PackedBwdArgs(C.Structure):
+    _fields_ = ([(n, _VP) for n in ("q", "k", "v", "o", "dout", "lse", "dq", "dk", "dv", "cu_q",
+                                    "cu_k")] +
+                [(n, _I) for n in ("n_seq", "Tq", "Tk", "Hq", "Hkv", "d")] +
+                [(n, _LL) for n in ("q_st", "q_sh", "k_st", "k_sh", "v_st", "v_sh", "o_st", "o_sh",
+                                    "do_st", "do_sh")] +
+                [("causal", _I), ("scale", _F), ("dtype", _I), ("workspace", _VP),
+                 ("workspace_bytes", _SZ), ("stream", _VP)])
+
+
 class PagedArgs(C.Structure):
     _fields_ = ([(n, _VP) for n in ("q", "k_pages", "v_pages", "o", "lse", "page_table", "kv_lens",
                                     "cu_q")] +
@@ -60,7 +71,8 @@ class PagedArgs(C.Structure):
 
 
 ENTRY_POINTS = {"blasst_rotary": RotaryArgs, "blasst_append": AppendArgs,
-                "blasst_packed_fwd": PackedArgs, "blasst_paged_fwd": PagedArgs}
+                "blasst_packed_fwd": PackedArgs, "blasst_packed_bwd": PackedBwdArgs,
+                "blasst_paged_fwd": PagedArgs}
 
 _dtypes = {}  # torch dtype -> blasst_dtype
 _calls = {}   # entry point -> bound C function
@@ -76,6 +88,8 @@ def _bind():
         _calls[name] = f
     lib.blasst_seq_workspace_bytes.argtypes = [_I]
     lib.blasst_seq_workspace_bytes.restype = _SZ
+    lib.blasst_packed_bwd_workspace_bytes.argtypes = [_I] * 3
+    lib.blasst_packed_bwd_workspace_bytes.restype = _SZ
     _dtypes.update({torch.bfloat16: BLASST_BF16, torch.float32: BLASST_FP32,
                     torch.float16: BLASST_FP16})
     return lib
@@ -186,6 +200,14 @@ def blasst_seq_workspace_bytes(d: int) -> int:
         _bind()
     from . import load_library
     return int(load_library().blasst_seq_workspace_bytes(int(d)))
+
+
+def blasst_packed_bwd_workspace_bytes(Tq: int, Hq: int, Hkv: int) -> int:
+    """The C entry point of the same name."""
+    if not _calls:
+        _bind()
+    from . import load_library
+    return int(load_library().blasst_packed_bwd_workspace_bytes(int(Tq), int(Hq), int(Hkv)))
 
 
 _ws_bytes = {}  # (device, d) -> bytes
@@ -377,6 +399,46 @@ def attention_packed(q, k, v, cu_q, cu_k=None, *, causal=True, scale=0.0, worksp
         _index(cu_q, "cu_q"), _index(cu_k, "cu_k", n + 1), n, Tq, Tk, Hq, Hkv, d, *_strides(q),
         *_strides(k), *_strides(v), int(bool(causal)), scale, dt, ws.data_ptr(), nbytes, s))
     return o, lse
+
+
+@_on
+def attention_packed_backward(q, k, v, o, lse, dout, cu_q, cu_k=None, *, causal=True, scale=0.0,
+                              workspace=None, stream=None):
+    """blasst_packed_bwd: gradients (dq, dk, dv) of ``attention_packed`` in the
+    inputs' type, from its outputs o and lse and the gradient dout of o. Tokens
+    of no sequence are left unwritten."""
+    import torch
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (o, "o"), (dout, "dout")):
+        _rows(t, name)
+    dt = _dtype(q, k, v, o, dout)
+    Tq, Hq, d = q.shape
+    Tk, Hkv, dk_ = k.shape
+    if dk_ != d or v.shape != k.shape:
+        raise ValueError("k and v must be [Tk, Hkv, d] with q's d")
+    if o.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("o and dout must have q's shape")
+    if lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 tensor [Tq, Hq]")
+    n = cu_q.shape[0] - 1
+    if cu_k is None:
+        cu_k = cu_q
+    dq = torch.empty((Tq, Hq, d), dtype=q.dtype, device=q.device)
+    dk = torch.empty((Tk, Hkv, d), dtype=q.dtype, device=q.device)
+    dv = torch.empty((Tk, Hkv, d), dtype=q.dtype, device=q.device)
+    made = None
+    if workspace is None:
+        nbytes = max(16, blasst_packed_bwd_workspace_bytes(Tq, Hq, Hkv))
+        workspace = made = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    s = _stream_of(stream, dq, dk, dv, made)
+    _call("blasst_packed_bwd", PackedBwdArgs(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(), lse.data_ptr(),
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _index(cu_q, "cu_q"),
+        _index(cu_k, "cu_k", n + 1), n, Tq, Tk, Hq, Hkv, d, *_strides(q), *_strides(k), *_strides(v),
+        *_strides(o), *_strides(dout), int(bool(causal)), scale, dt, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), s))
+    return dq, dk, dv
 
 
 @_on

@@ -459,6 +459,46 @@ typedef struct blasst_packed_args {
 } blasst_packed_args;
 BLASST_API int blasst_packed_fwd(const blasst_packed_args* args);
 
+/* Gradients of blasst_packed_fwd: with P = exp(scale q.k - lse) on the visible
+ * pairs, D = rowsum(dout * o) and dS = P * (dout.v - D),
+ *     dq = scale dS K,  dk = scale dS^T Q,  dv = P^T dout,
+ * dk and dv summed over the query heads of a KV head. The same inputs give the
+ * same bits: every output row is summed by one block in one order.
+ *   q, k, v     as in the forward; o, dout [Tq, Hq, d] by strides; lse [Tq, Hq]
+ *               contiguous, the forward's for these inputs.
+ *   dq [Tq, Hq, d], dk, dv [Tk, Hkv, d]: contiguous, in the inputs' type. Rows
+ *               without keys get dq = 0, keys without queries dk = dv = 0;
+ *               tokens of no sequence are left as they were.
+ *   workspace   >= blasst_packed_bwd_workspace_bytes(Tq, Hq, Hkv) bytes, not
+ *               shared by calls that may run at the same time.
+ * Other arguments as in blasst_packed_fwd. */
+typedef struct blasst_packed_bwd_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* o;
+  const void* dout;
+  const float* lse;
+  void* dq;
+  void* dk;
+  void* dv;
+  const int* cu_q;
+  const int* cu_k;
+  int n_seq, Tq, Tk, Hq, Hkv, d;
+  long long q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh, do_st, do_sh;
+  int causal;
+  float scale;
+  int dtype;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+} blasst_packed_bwd_args;
+BLASST_API int blasst_packed_bwd(const blasst_packed_bwd_args* args);
+
+/* Workspace bytes of blasst_packed_bwd: two fp32 statistics per query row and
+ * 16 bytes per KV head (0 for arguments out of range). Host only. */
+BLASST_API size_t blasst_packed_bwd_workspace_bytes(int Tq, int Hq, int Hkv);
+
 /* Attention of new tokens (a chunk, or one per sequence) over the paged cache,
  * exact. kv_lens[s] counts the cached tokens with the new ones (already
  * written, e.g. by blasst_append); query token i of sequence s sees key j when
