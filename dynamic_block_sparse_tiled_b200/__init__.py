@@ -127,6 +127,10 @@ def load_library(path: str | None = None):
         lib.blasst_bwd.restype = i
         lib.blasst_bwd_workspace_bytes.argtypes = [i, i, i]
         lib.blasst_bwd_workspace_bytes.restype = sz
+        lib.blasst_seq_workspace_bytes.argtypes = [i]
+        lib.blasst_seq_workspace_bytes.restype = sz
+        lib.blasst_packed_bwd_workspace_bytes.argtypes = [i, i, i]
+        lib.blasst_packed_bwd_workspace_bytes.restype = sz
         lib.blasst_decode_workspace_bytes.argtypes = [i, i, i, i]
         lib.blasst_decode_workspace_bytes.restype = sz
         lib.blasst_decode.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, i, i, vp, sz, vp, vp, vp]

@@ -364,7 +364,9 @@ size_t blasst_seq_workspace_bytes(int d) {
 }
 
 int blasst_packed_fwd(const blasst_packed_args* a) {
-  if (!a || !a->q || !a->k || !a->v || !a->o || !a->lse || !a->cu_q || !a->cu_k) return BLASST_EINVAL;
+  // (a side without tokens has no pointers)
+  if (!a || !a->q || (a->Tk > 0 && (!a->k || !a->v)) || !a->o || !a->lse || !a->cu_q || !a->cu_k)
+    return BLASST_EINVAL;
   for (const void* ptr : {a->q, a->k, a->v, static_cast<const void*>(a->o),
                           static_cast<const void*>(a->lse)})
     if (!aligned(ptr, 16)) return BLASST_EINVAL;
@@ -395,9 +397,12 @@ int blasst_packed_fwd(const blasst_packed_args* a) {
   p.Hkv = a->Hkv;
   p.g = a->Hq / a->Hkv;
   p.causal = a->causal ? 1 : 0;
+  // a map needs an address also where no tile is ever loaded
+  const void* k = a->Tk > 0 ? a->k : a->q;
+  const void* v = a->Tk > 0 ? a->v : a->q;
   CUtensorMap mk, mv;
-  if (!make_map4(&mk, a->k, a->dtype, {a->d, a->Tk, a->Hkv, 1}, {a->k_st, a->k_sh, 8}, 128, 1) ||
-      !make_map4(&mv, a->v, a->dtype, {a->d, a->Tk, a->Hkv, 1}, {a->v_st, a->v_sh, 8}, 128, 1))
+  if (!make_map4(&mk, k, a->dtype, {a->d, a->Tk, a->Hkv, 1}, {a->k_st, a->k_sh, 8}, 128, 1) ||
+      !make_map4(&mv, v, a->dtype, {a->d, a->Tk, a->Hkv, 1}, {a->v_st, a->v_sh, 8}, 128, 1))
     return BLASST_ECUDA;
   return run_seq(p, a->q, a->q_st, a->q_sh, a->d, a->scale, a->dtype, mk, mv, a->workspace, sms,
                  a->stream);
@@ -409,9 +414,9 @@ size_t blasst_packed_bwd_workspace_bytes(int Tq, int Hq, int Hkv) {
 }
 
 int blasst_packed_bwd(const blasst_packed_bwd_args* a) {
-  if (!a || !a->q || !a->k || !a->v || !a->o || !a->dout || !a->lse || !a->dq || !a->dk || !a->dv ||
-      !a->cu_q || !a->cu_k)
-    return BLASST_EINVAL;
+  if (!a || !a->cu_q || !a->cu_k) return BLASST_EINVAL;
+  if (a->Tq > 0 && (!a->q || !a->o || !a->dout || !a->lse || !a->dq)) return BLASST_EINVAL;
+  if (a->Tk > 0 && (!a->k || !a->v || !a->dk || !a->dv)) return BLASST_EINVAL;
   for (const void* ptr : {a->q, a->k, a->v, a->o, a->dout, static_cast<const void*>(a->lse),
                           static_cast<const void*>(a->dq), static_cast<const void*>(a->dk),
                           static_cast<const void*>(a->dv)})
@@ -483,13 +488,18 @@ int blasst_packed_bwd(const blasst_packed_bwd_args* a) {
   r.row_blocks = static_cast<int>((static_cast<long long>(a->Tq) * p.g + blasst::kBwdRowsPerBlock - 1) /
                                   blasst::kBwdRowsPerBlock);
   r.shift = shift;
+  // a map needs an address also where no tile is ever loaded
+  const void* q = a->Tq > 0 ? a->q : a->k;
+  const void* dout = a->Tq > 0 ? a->dout : a->k;
+  const void* k = a->Tk > 0 ? a->k : a->q;
+  const void* v = a->Tk > 0 ? a->v : a->q;
   CUtensorMap mq, mdo, mk, mv;
-  if (!make_map4(&mq, a->q, a->dtype, {a->d, p.g, a->Tq, a->Hkv}, {a->q_sh, a->q_st, a->q_sh * p.g},
+  if (!make_map4(&mq, q, a->dtype, {a->d, p.g, a->Tq, a->Hkv}, {a->q_sh, a->q_st, a->q_sh * p.g},
                  p.g, p.rt) ||
-      !make_map4(&mdo, a->dout, a->dtype, {a->d, p.g, a->Tq, a->Hkv},
+      !make_map4(&mdo, dout, a->dtype, {a->d, p.g, a->Tq, a->Hkv},
                  {a->do_sh, a->do_st, a->do_sh * p.g}, p.g, p.rt) ||
-      !make_map4(&mk, a->k, a->dtype, {a->d, a->Tk, a->Hkv, 1}, {a->k_st, a->k_sh, 8}, 128, 1) ||
-      !make_map4(&mv, a->v, a->dtype, {a->d, a->Tk, a->Hkv, 1}, {a->v_st, a->v_sh, 8}, 128, 1))
+      !make_map4(&mk, k, a->dtype, {a->d, a->Tk, a->Hkv, 1}, {a->k_st, a->k_sh, 8}, 128, 1) ||
+      !make_map4(&mv, v, a->dtype, {a->d, a->Tk, a->Hkv, 1}, {a->v_st, a->v_sh, 8}, 128, 1))
     return BLASST_ECUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(a->stream);
   if (!f16)
