@@ -248,11 +248,9 @@ __global__ void __launch_bounds__(384, 1)
     for (int s0 = 0; s0 < p.n_seq && it.kind == 0 && live; s0 += 32) {
       const int i = s0 + lane;
       const int s = key ? i : p.n_seq - 1 - i;
-      int tiles = 0;
-      if (i < p.n_seq) {
-        const SeqSpan q = span(s);
-        tiles = key ? (q.kvlen + C::BK - 1) / C::BK : q.tiles;
-      }
+      SeqSpan mine{};
+      if (i < p.n_seq) mine = span(s);
+      const int tiles = key ? (mine.kvlen + C::BK - 1) / C::BK : mine.tiles;
       int upto = tiles;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -264,8 +262,7 @@ __global__ void __launch_bounds__(384, 1)
         const int l = __ffs(hit) - 1;
         const int n = __shfl_sync(0xffffffffu, tiles, l);
         const int start = before + __shfl_sync(0xffffffffu, upto, l) - n;
-        const int i_hit = s0 + l;
-        const SeqSpan q = span(key ? i_hit : p.n_seq - 1 - i_hit);
+        const SeqSpan q = seq_span_of(mine, l);
         it.hk = h;
         it.q0 = q.q0;
         it.qlen = q.qlen;

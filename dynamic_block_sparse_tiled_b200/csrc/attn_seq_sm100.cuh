@@ -17,7 +17,17 @@
 //              each K and V block once it is in shared memory;
 //   one tile   (up to 128 rows, e.g. single tokens): both streams own the same
 //              rows and take the even and the odd key blocks; their sums are
-//              joined from TMEM at the end.
+//              joined from TMEM at the end;
+//   few rows   (one tile of up to 32 rows): the rows are repeated in the four
+//              quarters of the TMEM lanes and quarter i takes the keys
+//              [32 i, 32 i + 32) of a block (P is 0 elsewhere), so that all
+//              four warps of a stream take exponentials; their sums are joined
+//              through shared memory at the end. With one warp's 128 columns a
+//              block took 2800 cycles of that warp and a step of single tokens
+//              was bound by it (855 us for 4.3 GB of cached keys and values).
+//              In a kernel of its own (FEW, which takes any item): beside the
+//              others' block loop it made the compiler spill there (3.5 -> 6.2
+//              ms for 32768 prompt tokens of 32 heads).
 // Warps 0-3, 4-7: softmax of stream 0, 1 (thread = row = TMEM lane); warp 8:
 // TMA producer; warp 9: tcgen05 issuer; warp 10: finds the CTA's items and
 // hands the others one record each (11 only fills the warpgroup, which gives
@@ -54,9 +64,11 @@ struct SeqAttnParams {
   long long table_stride;
   int table_width;
   int page_size, n_pages;
-  int chunk;  // keys per TMA box: 128, or the largest power of two that divides page_size
+  // keys per TMA box, a power of two: 128, or the largest that divides page_size
+  int chunk_log2;
   int n_seq, Tq, Tk, Hq, Hkv, g;
   int rt;        // tokens per 128-row tile
+  int rt_few;    // tokens per 32 rows (0: a group is larger)
   int n_tiles;   // most tiles per KV head (one item per CTA); 0: shared list
   int causal;
   float scale_log2;
@@ -102,6 +114,18 @@ __device__ __forceinline__ SeqSpan seq_span(const int* cu_q, const int* cu_k, co
   return r;
 }
 
+// Lane l's span, to all lanes.
+__device__ __forceinline__ SeqSpan seq_span_of(const SeqSpan& q, int l) {
+  SeqSpan r;
+  r.q0 = __shfl_sync(0xffffffffu, q.q0, l);
+  r.qlen = __shfl_sync(0xffffffffu, q.qlen, l);
+  r.k0 = __shfl_sync(0xffffffffu, q.k0, l);
+  r.kvlen = __shfl_sync(0xffffffffu, q.kvlen, l);
+  r.off = r.kvlen - r.qlen;
+  r.tiles = __shfl_sync(0xffffffffu, q.tiles, l);
+  return r;
+}
+
 template <int D>
 struct SeqAttnCfg {
   static constexpr int NTHREADS = 384;
@@ -127,7 +151,8 @@ struct SeqAttnCfg {
   static constexpr int B_DONE = B_P + 2;    // every product of the item done
   static constexpr int B_OFREE = B_DONE + 1;  // O read (8 warps)
   static constexpr int B_ML = B_OFREE + 1;  // (m, l) of both streams of a one-tile item (8 warps)
-  static constexpr int B_DRAIN = B_ML + 1;
+  static constexpr int B_X = B_ML + 1;      // few rows: sums in shared memory (8 warps)
+  static constexpr int B_DRAIN = B_X + 1;
   static constexpr int NITEM = 2;
   static constexpr int B_IF = B_DRAIN + 1;   // [NITEM] item record written
   static constexpr int B_IE = B_IF + NITEM;  // [NITEM] read (loader, issuer, 8 softmax warps)
@@ -193,9 +218,10 @@ __device__ __forceinline__ int seq_first_block(long long at, const SeqItem& it, 
 // sees (causal), or the sequence's length. seq < 0 ends.
 struct SeqRecord {
   static constexpr int kWords = 12;
-  static constexpr int kOne = 1, kWhole = 2, kBegins = 4;
+  static constexpr int kOne = 1, kWhole = 2, kBegins = 4, kFew = 8;
   int hk, qtok, ntok, b0, nb, cnt0, kvlen, k0, vis, seq, mode;
   __device__ __forceinline__ bool one() const { return mode & kOne; }
+  __device__ __forceinline__ bool few() const { return mode & kFew; }
   __device__ __forceinline__ int cnt(int st) const {
     return st == 0 ? cnt0 : (one() ? nb >> 1 : nb);
   }
@@ -222,9 +248,53 @@ struct SeqType<__half> {
   static constexpr uint32_t kFormat = 0;
 };
 
+// Few rows: a lane's sums of both streams over half of the columns, weighted,
+// to shared memory; a weight of 0 takes nothing (the sum may never have been
+// written).
+template <int D>
+__device__ __forceinline__ void seq_few_put(uint32_t o_tm, float* x, float w0, float w1) {
+#pragma unroll 1
+  for (int c = 0; c < D / 64; ++c) {
+    uint32_t r0[32], r1[32];
+    ptx::tmem_ld32(o_tm + 32 * c, r0);
+    ptx::tmem_ld32(o_tm + D + 32 * c, r1);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float a = w0 == 0.0f ? 0.0f : w0 * __uint_as_float(r0[j]);
+      x[(32 * c + j) * 32] = w1 == 0.0f ? a : fmaf(w1, __uint_as_float(r1[j]), a);
+    }
+  }
+}
+
+// Adds up the four quarters' sums of a row over D / 8 columns; to `part`
+// (fp32) if there is one, else to `o`.
 template <int D, typename T>
+__device__ __forceinline__ void seq_few_take(const float* x, T* o, float* part) {
+  constexpr int Q = D / 2 * 32;
+#pragma unroll 1
+  for (int c = 0; c < D / 64; ++c) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float* y = x + (8 * c + j) * 32;
+      v[j] = (y[0] + y[Q]) + (y[2 * Q] + y[3 * Q]);
+    }
+    if (part) {
+      reinterpret_cast<float4*>(part + 8 * c)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(part + 8 * c)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      *reinterpret_cast<uint4*>(o + 8 * c) =
+          make_uint4(seq_pack2<T>(v[0], v[1]), seq_pack2<T>(v[2], v[3]), seq_pack2<T>(v[4], v[5]),
+                     seq_pack2<T>(v[6], v[7]));
+    }
+  }
+}
+
+template <int D, typename T, bool FEW>
 __global__ void __launch_bounds__(384, 1)
     blasst_seq_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
+                           const __grid_constant__ CUtensorMap tmQFew,
                            const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const SeqAttnParams p) {
   using C = SeqAttnCfg<D>;
@@ -264,6 +334,7 @@ __global__ void __launch_bounds__(384, 1)
     ptx::mbar_init(bar(C::B_DONE), 1);
     ptx::mbar_init(bar(C::B_OFREE), 8);
     ptx::mbar_init(bar(C::B_ML), 8);
+    ptx::mbar_init(bar(C::B_X), 8);
     ptx::mbar_init(bar(C::B_DRAIN), 1);
     for (int i = 1; i < 4; ++i) misc[i] = 0;
     ptx::fence_mbar_init();
@@ -303,6 +374,7 @@ __global__ void __launch_bounds__(384, 1)
     seq_record_error(p.err, BLASST_ETIMEOUT);
   };
 
+  ptx::grid_launch_dependents();  // the join's blocks may come up meanwhile
   if (warp >= 8) {
    ptx::reg_give<C::REGS_REST>();
    if (warp == C::WARP_ITEM) {
@@ -310,6 +382,7 @@ __global__ void __launch_bounds__(384, 1)
     const int kv_cap = static_cast<int>(
         min(static_cast<long long>(p.table_width) * p.page_size, 0x7fffff00ll));
     auto span = [&](int s) -> SeqSpan {
+      if (s < 0 || s >= p.n_seq) return SeqSpan{};
       return seq_span(p.cu_q, p.cu_k, p.kv_lens, kv_cap, p.Tq, p.Tk, 2 * p.rt, s, p.err);
     };
     int n = 0;
@@ -334,6 +407,7 @@ __global__ void __launch_bounds__(384, 1)
         w[8] = p.causal ? q.off + it.tok0 + 1 : q.kvlen;
         w[9] = s;
         w[10] = (it.one ? SeqRecord::kOne : 0) | (whole ? SeqRecord::kWhole : 0) |
+                (FEW && it.one && it.ntok <= p.rt_few ? SeqRecord::kFew : 0) |
                 (b0 == 0 ? SeqRecord::kBegins : 0);
         ptx::mbar_arrive(bar(C::B_IF + slot));
       }
@@ -350,9 +424,8 @@ __global__ void __launch_bounds__(384, 1)
       int before = 0;
       bool found = false;
       for (int s0 = p.n_seq - 1; s0 >= 0 && !found && live; s0 -= 32) {
-        const int s = s0 - lane;
-        const int tiles = s >= 0 ? span(s).tiles : 0;
-        int upto = tiles;
+        const SeqSpan mine = span(s0 - lane);
+        int upto = mine.tiles;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const int v = __shfl_up_sync(0xffffffffu, upto, d);
@@ -362,7 +435,7 @@ __global__ void __launch_bounds__(384, 1)
         if (hit) {
           const int l = __ffs(hit) - 1;
           const int end = before + __shfl_sync(0xffffffffu, upto, l);
-          const SeqSpan q = span(s0 - l);
+          const SeqSpan q = seq_span_of(mine, l);
           const SeqItem it = seq_item(q, p.causal, p.rt, end - 1 - want);
           ok = put(s0 - l, q, h, it, 0, it.nblk);
           found = true;
@@ -373,15 +446,28 @@ __global__ void __launch_bounds__(384, 1)
       // ---- this CTA's range of the shared list -----------------------------
       // no item cut at the range's end, until one is found
       if (lane == 0) p.part_desc[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
-      long long total = 0;
+      // the sequences' spans are read 32 at a time, one per lane; up to 32 of
+      // them are read once
+      int chunk = -1;
+      SeqSpan mine;
+      auto load_chunk = [&](int s0) {
+        if (s0 == chunk) return;
+        mine = span(s0 + lane);
+        chunk = s0;
+      };
+      auto span_of = [&](int s) -> SeqSpan {
+        load_chunk(s & ~31);
+        return seq_span_of(mine, s & 31);
+      };
+      long long total = 0, own = 0;
       for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
-        const int s = s0 + lane;
-        long long c = s < p.n_seq ? seq_cost(span(s), p.causal, p.rt) : 0;
+        load_chunk(s0);
+        own = seq_cost(mine, p.causal, p.rt) * p.Hkv;
+        long long c = own;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
         total += c;
       }
-      total *= p.Hkv;
       const long long share = (total + gridDim.x - 1) / gridDim.x;
       const long long range = share < kSeqMinRange ? kSeqMinRange : share;
       const long long lo = range * blockIdx.x;
@@ -390,8 +476,10 @@ __global__ void __launch_bounds__(384, 1)
       int s = 0, h = 0, t = 0;
       bool found = false;
       for (int s0 = 0; s0 < p.n_seq && !found && live && lo < total; s0 += 32) {
-        const int sl = s0 + lane;
-        const long long own = sl < p.n_seq ? seq_cost(span(sl), p.causal, p.rt) * p.Hkv : 0;
+        if (s0 != chunk) {
+          load_chunk(s0);
+          own = seq_cost(mine, p.causal, p.rt) * p.Hkv;
+        }
         long long upto = own;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -412,7 +500,7 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
       if (found) {
-        SeqSpan q = span(s);
+        SeqSpan q = span_of(s);
         while (at < hi && ok) {
           const SeqItem it = seq_item(q, p.causal, p.rt, t);
           const long long end = at + kSeqItemCost + static_cast<long long>(it.nblk) * it.unit;
@@ -439,7 +527,7 @@ __global__ void __launch_bounds__(384, 1)
               h = 0;
               do {
                 if (++s >= p.n_seq) break;
-                q = span(s);
+                q = span_of(s);
               } while (q.tiles == 0);
               if (s >= p.n_seq) break;
             }
@@ -460,13 +548,24 @@ __global__ void __launch_bounds__(384, 1)
       ptx::prefetch_tmap(&tmK);
       ptx::prefetch_tmap(&tmV);
     }
-    const int nch = C::BK / p.chunk;
+    // (no divisions in the loop over loads: this warp's own time per load is
+    // what a step of single tokens was bound by, 1.03 ms -> see below)
+    const int chunk = 1 << p.chunk_log2;
+    const int nch_log2 = 7 - p.chunk_log2, nch = 1 << nch_log2;
     const int q_box_rows = p.g * p.rt;
+    // Places in the cache (page, row in it) are looked up a group of 32 chunks
+    // (one per lane) at a time, one group ahead of their use: the groups
+    // before, at and behind the newest K block (V follows one block later).
+    const int group_log2 = 5 - nch_log2;  // blocks of a group
+    int2 at_before = make_int2(0, 0), at_now = at_before, at_next = at_before;
+    int group = -1;
     uint32_t ring = 0;   // loads issued
+    uint32_t slot = 0, turn = 0;  // of the ring; turn: parity of the slot's phase
     uint32_t tails = 0;  // cleared last blocks
     bool ok = true;
     bool last_tail = false;
     int q_loads = 0;
+    bool few_before = false;
     SeqRecord it;
     for (int n = 0; ok; ++n) {
       ok = __all_sync(0xffffffffu, next_item(n, it)) != 0;
@@ -475,15 +574,38 @@ __global__ void __launch_bounds__(384, 1)
       if (it.seq < 0) break;
       const int nb = it.nb;
       const int nload = 2 * nb;
+      auto read_group = [&](int gr) -> int2 {
+        const long long key = (static_cast<long long>(gr) * 32 + lane) << p.chunk_log2;
+        if (key >= it.kvlen) return make_int2(p.n_pages, 0);
+        const int k = static_cast<int>(key);
+        return make_int2(p.table[static_cast<long long>(it.seq) * p.table_stride + k / p.page_size],
+                         k % p.page_size);
+      };
+      if (p.table) {
+        group = it.b0 >> group_log2;
+        at_now = read_group(group);
+        at_next = read_group(group + 1);
+      }
       const int q_at = n == 0 ? 0 : (nb >= 2 ? 3 : min(1, nload));
       for (int r = 0; r <= nload && ok; ++r) {
         if (r == q_at) {
           // Q, once the item before has finished with it (its first K and V
-          // do not wait for that)
+          // do not wait for that); few rows leave their sums in Q's place
           if (lane == 0) {
             if (n > 0)
               ok = ptx::mbar_wait(bar(C::B_DONE), (n - 1) & 1, abort_flag, p.timeout_ns);
-            if (ok) {
+            // (only behind the wait above is the phase before known to be over)
+            if (FEW && ok && few_before)
+              ok = ptx::mbar_wait(bar(C::B_OFREE), (n - 1) & 1, abort_flag, p.timeout_ns);
+            if (FEW && ok && it.few()) {
+              ptx::mbar_arrive_expect_tx(bar(C::B_Q), 4 * C::DBOX * p.g * p.rt_few * 128);
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int x = 0; x < C::DBOX; ++x)
+                  ptx::tma_load_4d(sb + C::OFF_Q + x * C::BOX + i * 32 * 128, &tmQFew, x * 64, 0,
+                                   it.qtok, it.hk, bar(C::B_Q));
+              q_loads = n + 1;
+            } else if (ok) {
               const int tiles = it.one() ? 1 : 2;
               ptx::mbar_arrive_expect_tx(bar(C::B_Q), tiles * C::DBOX * q_box_rows * 128);
               for (int i = 0; i < tiles; ++i)
@@ -495,6 +617,7 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          few_before = it.few();
         }
         if (r == nload || !ok) break;
         // the order in which the issuer takes the blocks
@@ -517,28 +640,34 @@ __global__ void __launch_bounds__(384, 1)
         const int valid = min(C::BK, it.kvlen - key0);
         // this lane's piece of the block
         int row = it.k0 + key0, page = 0;
-        const bool mine = lane < nch && lane * p.chunk < valid;
-        if (p.table && mine) {
-          const int key = key0 + lane * p.chunk;
-          row = key % p.page_size;
-          page = p.table[static_cast<long long>(it.seq) * p.table_stride + key / p.page_size];
-          if (page < 0 || page >= p.n_pages) {
+        const bool mine = lane < nch && (lane << p.chunk_log2) < valid;
+        if (p.table) {
+          const int block = it.b0 + b;
+          if ((block >> group_log2) > group) {  // K moves on
+            ++group;
+            at_before = at_now;
+            at_now = at_next;
+            at_next = read_group(group + 1);
+          }
+          const bool now = (block >> group_log2) == group;
+          const int from = ((block & ((1 << group_log2) - 1)) << nch_log2) + (lane & (nch - 1));
+          page = __shfl_sync(0xffffffffu, now ? at_now.x : at_before.x, from);
+          row = __shfl_sync(0xffffffffu, now ? at_now.y : at_before.y, from);
+          if (mine && static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages)) {
             seq_record_error(p.err, BLASST_EINDEX);
             page = p.n_pages;  // outside the map: zeros
           }
         }
-        const uint32_t st = ring % C::NST;
+        const uint32_t st = slot;
         const uint32_t full = bar(C::B_KVF + st);
         const bool tail = is_v && valid < C::BK;
         const uint32_t fb = tail ? bar(C::B_TAIL) : full;
         if (lane == 0) {
           if (ring >= C::NST)
-            ok = ptx::mbar_wait(bar(C::B_KVE + st), ((ring / C::NST) - 1) & 1, abort_flag,
-                                p.timeout_ns);
-          if (ok) {
-            const int pieces = (valid + p.chunk - 1) / p.chunk;
-            ptx::mbar_arrive_expect_tx(fb, pieces * p.chunk * 128 * C::DBOX);
-          }
+            ok = ptx::mbar_wait(bar(C::B_KVE + st), turn ^ 1u, abort_flag, p.timeout_ns);
+          if (ok)
+            ptx::mbar_arrive_expect_tx(fb, ((valid + chunk - 1) >> p.chunk_log2 << p.chunk_log2) *
+                                               (128 * C::DBOX));
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok) break;
@@ -547,9 +676,13 @@ __global__ void __launch_bounds__(384, 1)
           const CUtensorMap* tm = is_v ? &tmV : &tmK;
 #pragma unroll
           for (int x = 0; x < C::DBOX; ++x)
-            ptx::tma_load_4d(dst + x * C::BOX + lane * p.chunk * 128, tm, x * 64, row, it.hk, page, fb);
+            ptx::tma_load_4d(dst + x * C::BOX + (lane << p.chunk_log2) * 128, tm, x * 64, row, it.hk, page, fb);
         }
         ++ring;
+        if (++slot == C::NST) {
+          slot = 0;
+          turn ^= 1u;
+        }
         last_tail = tail;
         if (tail) {
           // Rows behind the sequence's end (a neighbour's, a page's leftovers,
@@ -667,7 +800,6 @@ __global__ void __launch_bounds__(384, 1)
     const int st = warp >> 2;
     const int quad = warp & 3;
     const int row = quad * 32 + lane;  // row of the tile, TMEM lane
-    const int row_tok = row / p.g, row_head = row % p.g;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_tm = tmem + lane_base + C::S_COL + st * 128;
     const uint32_t o_tm = tmem + lane_base + C::O_COL + st * D;
@@ -681,93 +813,153 @@ __global__ void __launch_bounds__(384, 1)
       if (lane == 0) r = ptx::mbar_wait(b, parity, abort_flag, p.timeout_ns);
       return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
     };
+    // S of a block is issued behind the P V of the one before: O is quiet until
+    // P is handed on
+    auto scale_o = [&](float alpha) {
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        ptx::tmem_ld32(o_tm + 32 * c, r);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+        ptx::tmem_st32(o_tm + 32 * c, r);
+      }
+    };
+    uint32_t fews = 0;  // items of few rows done
     SeqRecord it;
     for (int n = 0; ok; ++n) {
       ok = __all_sync(0xffffffffu, next_item(n, it)) != 0;
       if (!ok) break;
       if (lane == 0) item_read(n);
       if (it.seq < 0) break;
-      const bool one = it.one();
+      const bool one = it.one(), few = FEW && it.few();
       const int cnt = it.cnt(st);
       const int first_tok = one ? 0 : st * p.rt;
+      const int row_tok = (few ? lane : row) / p.g, row_head = (few ? lane : row) % p.g;
       const int tok = first_tok + row_tok;  // of the item
-      const bool exists = row_tok < p.rt && tok < it.ntok;
+      const bool exists = row_tok < (few ? p.rt_few : p.rt) && tok < it.ntok;
       const bool active = __any_sync(0xffffffffu, exists) != 0;
       // keys below `limit` are visible; the tile's first token sees the fewest
       const int limit = p.causal ? min(it.vis + tok, it.kvlen) : it.kvlen;
       const int least = p.causal ? min(it.vis + first_tok, it.kvlen) : it.kvlen;
       float mref = -INFINITY, l = 0.0f;
-      for (int i = 0; i < cnt; ++i) {
-        const int col0 = (it.b0 + (one ? 2 * i + st : i)) * C::BK;
-        ok = lane0_wait(bar(C::B_S + st), steps & 1);
-        ++steps;
-        if (!ok) break;
-        ptx::tc_fence_after();
-        if (active) {
-          uint32_t sv[128];
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          const bool cut = col0 + C::BK > least;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) ptx::tmem_ld32p(s_tm + 32 * c, sv + 32 * c);
+      if (few) {
+        for (int i = 0; i < cnt; ++i) {
+          const int col0 = (it.b0 + (one ? 2 * i + st : i)) * C::BK;
+          ok = lane0_wait(bar(C::B_S + st), steps & 1);
+          ++steps;
+          if (!ok) break;
+          ptx::tc_fence_after();
+          // this quarter's 32 keys of the block
+          uint32_t sv[32];
+          ptx::tmem_ld32(s_tm + 32 * quad, sv);
           ptx::tmem_wait_ld();
-          if (cut) {
-            const int vis = limit - col0;
+          const int vis = limit - col0 - 32 * quad;
+          if (col0 + C::BK > least) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
+            for (int c = 0; c < 32; ++c)
               if (c >= vis) sv[c] = __float_as_uint(-INFINITY);
           }
+          float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 128; c += 8) {
+          for (int c = 0; c < 32; c += 4) {
             mx[0] = ptx::fmax3(mx[0], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
             mx[1] = ptx::fmax3(mx[1], __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
-            mx[2] = ptx::fmax3(mx[2], __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
-            mx[3] = ptx::fmax3(mx[3], __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
           }
-          const float mb = fmaxf(ptx::fmax3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
-          const bool need = mb > mref + C::TAU;  // the first keys of a row always move it
+          const float mb = fmaxf(mx[0], mx[1]) * sl2;
+          const bool need = mb > mref + C::TAU;
           if (__any_sync(0xffffffffu, need)) {
             const float mnew = need ? mb : mref;
-            const float alpha = need ? ptx::ex2(mref - mnew) : 1.0f;  // 0 from -inf
+            const float alpha = need ? ptx::ex2(mref - mnew) : 1.0f;
             mref = mnew;
             l *= alpha;
-            if (i > 0) {
-              // S of this block was issued behind the P V of the one before:
-              // O is quiet until P is handed on
-#pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t r[32];
-                ptx::tmem_ld32(o_tm + 32 * c, r);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
-                ptx::tmem_st32(o_tm + 32 * c, r);
-              }
-            }
+            if (i > 0) scale_o(alpha);
           }
           const float neg = mref == -INFINITY ? 0.0f : -mref;
-          float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          float rs[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t pk[16], zero[16];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              float x0, x1;
-              ptx::fma2(x0, x1, __uint_as_float(sv[32 * c + j]), __uint_as_float(sv[32 * c + j + 1]),
-                        sl2, sl2, neg, neg);
-              const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
-              const int a = j & 6;
-              ptx::add2(rs[a], rs[a + 1], rs[a], rs[a + 1], p0, p1);
-              pk[j / 2] = seq_pack2<T>(p0, p1);
-            }
-            ptx::tmem_st16(s_tm + 16 * c, pk);
+          for (int j = 0; j < 32; j += 2) {
+            float x0, x1;
+            ptx::fma2(x0, x1, __uint_as_float(sv[j]), __uint_as_float(sv[j + 1]), sl2, sl2, neg, neg);
+            const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+            const int a = j & 2;
+            ptx::add2(rs[a], rs[a + 1], rs[a], rs[a + 1], p0, p1);
+            pk[j / 2] = seq_pack2<T>(p0, p1);
+            zero[j / 2] = 0u;
           }
-          l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (q == quad) ptx::tmem_st16(s_tm + 16 * q, pk);
+            else ptx::tmem_st16(s_tm + 16 * q, zero);
+          }
+          l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
           ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(C::B_P + st));
         }
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(C::B_P + st));
+      } else {
+        for (int i = 0; i < cnt; ++i) {
+          const int col0 = (it.b0 + (one ? 2 * i + st : i)) * C::BK;
+          ok = lane0_wait(bar(C::B_S + st), steps & 1);
+          ++steps;
+          if (!ok) break;
+          ptx::tc_fence_after();
+          if (active) {
+            uint32_t sv[128];
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            const bool cut = col0 + C::BK > least;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ptx::tmem_ld32p(s_tm + 32 * c, sv + 32 * c);
+            ptx::tmem_wait_ld();
+            if (cut) {
+              const int vis = limit - col0;
+#pragma unroll
+              for (int c = 0; c < 128; ++c)
+                if (c >= vis) sv[c] = __float_as_uint(-INFINITY);
+            }
+#pragma unroll
+            for (int c = 0; c < 128; c += 8) {
+              mx[0] = ptx::fmax3(mx[0], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+              mx[1] = ptx::fmax3(mx[1], __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+              mx[2] = ptx::fmax3(mx[2], __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
+              mx[3] = ptx::fmax3(mx[3], __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
+            }
+            const float mb = fmaxf(ptx::fmax3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
+            const bool need = mb > mref + C::TAU;  // the first keys of a row always move it
+            if (__any_sync(0xffffffffu, need)) {
+              const float mnew = need ? mb : mref;
+              const float alpha = need ? ptx::ex2(mref - mnew) : 1.0f;  // 0 from -inf
+              mref = mnew;
+              l *= alpha;
+              if (i > 0) scale_o(alpha);
+            }
+            const float neg = mref == -INFINITY ? 0.0f : -mref;
+            float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                float x0, x1;
+                ptx::fma2(x0, x1, __uint_as_float(sv[32 * c + j]), __uint_as_float(sv[32 * c + j + 1]),
+                          sl2, sl2, neg, neg);
+                const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+                const int a = j & 6;
+                ptx::add2(rs[a], rs[a + 1], rs[a], rs[a + 1], p0, p1);
+                pk[j / 2] = seq_pack2<T>(p0, p1);
+              }
+              ptx::tmem_st16(s_tm + 16 * c, pk);
+            }
+            l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+            ptx::tmem_wait_st();
+          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(C::B_P + st));
+        }
       }
 
       // ---- the item's end ---------------------------------------------------
@@ -784,9 +976,20 @@ __global__ void __launch_bounds__(384, 1)
         if (!ok) break;
         const float2 a = ml[row], c = ml[128 + row];
         mref = fmaxf(a.x, c.x);
+        if (few) {
+          for (int q = 0; q < 4; ++q)
+            mref = ptx::fmax3(mref, ml[32 * q + lane].x, ml[128 + 32 * q + lane].x);
+        }
         w0 = a.x == -INFINITY ? 0.0f : ptx::ex2(a.x - mref);
         w1 = c.x == -INFINITY ? 0.0f : ptx::ex2(c.x - mref);
         l = a.y * w0 + c.y * w1;
+        if (few) {
+          l = 0.0f;
+          for (int q = 0; q < 8; ++q) {
+            const float2 b = ml[32 * q + lane];
+            if (b.x != -INFINITY) l = fmaf(b.y, ptx::ex2(b.x - mref), l);
+          }
+        }
       }
       ok = lane0_wait(bar(C::B_DONE), n & 1);
       ok = ok && *abort_flag == 0;
@@ -799,12 +1002,29 @@ __global__ void __launch_bounds__(384, 1)
       const bool whole = it.mode & SeqRecord::kWhole;
       const long long tok_row = static_cast<long long>(it.qtok + tok) * p.Hq + it.hk * p.g + row_head;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (it.mode & SeqRecord::kBegins ? 1 : 0);
-      const int prow = (one ? 0 : st * 128) + row;
+      const int prow = few ? lane : (one ? 0 : st * 128) + row;
       // one tile: each warpgroup takes half of the columns of both sums
       const int c_lo = one ? st * (D / 64) : 0;
       const int c_hi = one ? c_lo + D / 64 : D / 32;
       const bool second = one && it.nb > 1;
-      if (active) {
+      if (few) {
+        // each quarter's sums, [quarter][column][row] fp32, this warpgroup's
+        // half of the columns; then every warp adds up a quarter of those
+        constexpr int HALF = D / 2;
+        float* x = reinterpret_cast<float*>(smem + C::OFF_Q) + st * 4 * HALF * 32 + lane;
+        seq_few_put<D>(tmem + lane_base + C::O_COL + st * HALF, x + quad * HALF * 32,
+                       it.nb > 0 && l != 0.0f ? w0 * inv : 0.0f, second && l != 0.0f ? w1 * inv : 0.0f);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_X));
+        ok = lane0_wait(bar(C::B_X), fews & 1);
+        ++fews;
+        if (!ok) break;
+        if (exists) {
+          const int col = st * HALF + quad * (HALF / 4);
+          seq_few_take<D, T>(x + quad * (HALF / 4) * 32, static_cast<T*>(p.o) + tok_row * D + col,
+                             whole ? nullptr : p.part_o + (static_cast<size_t>(slot) * 256 + lane) * D + col);
+        }
+      } else if (active) {
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; ++c) {
           uint32_t r[32];
@@ -848,7 +1068,7 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
       }
-      if (exists && (st == 0 || !one)) {
+      if (exists && (st == 0 || !one) && (quad == 0 || !few)) {
         if (whole) p.lse[tok_row] = lse2 * 0.6931471805599453f;
         else p.part_lse[static_cast<size_t>(slot) * 256 + prow] = lse2;
       }
@@ -874,11 +1094,14 @@ __global__ void __launch_bounds__(384, 1)
 template <int D, typename T>
 __global__ void __launch_bounds__(256) blasst_seq_join_kernel(const SeqAttnParams p) {
   const int c = blockIdx.x;
+  ptx::grid_wait();
   const int4 d = p.part_desc[2 * c];
   if (d.x < 0) return;
   const int last = p.part_desc[2 * c + 1].x;
   const int lane = threadIdx.x & 31;
   constexpr int V = D / 32;  // columns per lane
+  // rows beyond the item's tokens have no place in o (few rows: rt_few < rt,
+  // but the tokens that exist are packed the same)
   const int rows = d.w ? 128 : 256;
   for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
     const int tok = (r >> 7) * p.rt + (r & 127) / p.g;

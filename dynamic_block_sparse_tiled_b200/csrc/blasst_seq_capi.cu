@@ -77,11 +77,11 @@ int check_regs(K kernel, int regs, int& known) {
   return known >= regs ? BLASST_OK : BLASST_EUNSUPPORTED;
 }
 
-template <int D, typename T>
-int launch_seq(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-               const blasst::SeqAttnParams& p, int sms, cudaStream_t stream) {
+template <int D, typename T, bool FEW>
+int launch_seq(const CUtensorMap& mq, const CUtensorMap& mq_few, const CUtensorMap& mk,
+               const CUtensorMap& mv, const blasst::SeqAttnParams& p, int sms, cudaStream_t stream) {
   using C = blasst::SeqAttnCfg<D>;
-  auto kernel = blasst::blasst_seq_attn_kernel<D, T>;
+  auto kernel = blasst::blasst_seq_attn_kernel<D, T, FEW>;
   static int regs = 0;  // of this instantiation
   if (const int rc = check_regs(kernel, C::REGS, regs)) return rc;
   cudaError_t e =
@@ -90,24 +90,44 @@ int launch_seq(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& 
   const bool shared_list = p.n_tiles == 0;
   const unsigned grid =
       shared_list ? static_cast<unsigned>(sms) : static_cast<unsigned>(p.n_tiles) * p.Hkv;
-  kernel<<<grid, C::NTHREADS, C::SMEM_BYTES, stream>>>(mq, mk, mv, p);
+  kernel<<<grid, C::NTHREADS, C::SMEM_BYTES, stream>>>(mq, mq_few, mk, mv, p);
   int rc = cuda_status(cudaGetLastError());
   if (rc != BLASST_OK || !shared_list) return rc;
-  blasst::blasst_seq_join_kernel<D, T><<<dim3(grid, 4), 256, 0, stream>>>(p);
-  return cuda_status(cudaGetLastError());
+  // launched while the first kernel runs, waits for its end itself
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t join{};
+  join.gridDim = dim3(grid, 4);
+  join.blockDim = dim3(256);
+  join.stream = stream;
+  join.attrs = &early;
+  join.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&join, blasst::blasst_seq_join_kernel<D, T>, p));
 }
+
+template <int D, typename T>
+int launch_seq_few(bool few, const CUtensorMap& mq, const CUtensorMap& mq_few, const CUtensorMap& mk,
+                   const CUtensorMap& mv, const blasst::SeqAttnParams& p, int sms, cudaStream_t stream) {
+  return few ? launch_seq<D, T, true>(mq, mq_few, mk, mv, p, sms, stream)
+             : launch_seq<D, T, false>(mq, mq_few, mk, mv, p, sms, stream);
+}
+
+constexpr long long kSeqFewKeys = 1024;
 
 // What the packed and the paged call share; `p` holds the keys' side already.
 int run_seq(blasst::SeqAttnParams& p, const void* q, long long q_st, long long q_sh, int d,
-            float scale, int dtype, const CUtensorMap& mk, const CUtensorMap& mv, void* workspace,
-            int sms, void* stream) {
+            float scale, int dtype, const CUtensorMap& mk, const CUtensorMap& mv,
+            long long most_keys, void* workspace, int sms, void* stream) {
   p.rt = 128 / p.g;
-  // One item per CTA once the tiles fill the GPU several times: their order
-  // then shares K and V in L2. Fewer tiles, or mostly single tokens: the
-  // shared list, which cuts long rows of key blocks between SMs.
+  // One item per CTA once the tiles fill the GPU several times (their order
+  // then shares K and V in L2), or if no sequence can have many keys (nothing
+  // worth cutting, and no second kernel). Fewer tiles, or mostly single tokens:
+  // the shared list, which cuts long rows of key blocks between SMs.
   const long long full = static_cast<long long>(p.Tq) / (2 * p.rt);
   const long long tiles = std::min<long long>(p.Tq, full + p.n_seq);
-  p.n_tiles = full * p.Hkv >= 8ll * sms && tiles * p.Hkv < 0x7fffffffll ? static_cast<int>(tiles) : 0;
+  const bool single = full * p.Hkv >= 8ll * sms || most_keys <= kSeqFewKeys;
+  p.n_tiles = single && tiles * p.Hkv < 0x7fffffffll ? static_cast<int>(tiles) : 0;
   const size_t rows = static_cast<size_t>(sms) * 2 * 256;
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = p.part_o + rows * d;
@@ -115,15 +135,20 @@ int run_seq(blasst::SeqAttnParams& p, const void* q, long long q_st, long long q
   const double sc = scale > 0.0f ? static_cast<double>(scale) : 1.0 / std::sqrt(static_cast<double>(d));
   p.scale_log2 = static_cast<float>(sc * 1.4426950408889634);
   p.timeout_ns = kTimeoutNs;
-  CUtensorMap mq;
-  if (!make_map4(&mq, q, dtype, {d, p.g, p.Tq, p.Hkv}, {q_sh, q_st, q_sh * p.g}, p.g, p.rt))
+  p.rt_few = p.g <= 32 ? 32 / p.g : 0;
+  CUtensorMap mq, mq_few;
+  if (!make_map4(&mq, q, dtype, {d, p.g, p.Tq, p.Hkv}, {q_sh, q_st, q_sh * p.g}, p.g, p.rt) ||
+      !make_map4(&mq_few, q, dtype, {d, p.g, p.Tq, p.Hkv}, {q_sh, q_st, q_sh * p.g}, p.g,
+                 std::max(1, p.rt_few)))
     return BLASST_ECUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // the kernel for few rows when the sequences have up to 32 rows on average
+  const bool few = p.rt_few > 0 && static_cast<long long>(p.Tq) * p.g <= 32ll * p.n_seq;
   if (dtype == BLASST_BF16)
-    return d == 128 ? launch_seq<128, __nv_bfloat16>(mq, mk, mv, p, sms, s)
-                    : launch_seq<64, __nv_bfloat16>(mq, mk, mv, p, sms, s);
-  return d == 128 ? launch_seq<128, __half>(mq, mk, mv, p, sms, s)
-                  : launch_seq<64, __half>(mq, mk, mv, p, sms, s);
+    return d == 128 ? launch_seq_few<128, __nv_bfloat16>(few, mq, mq_few, mk, mv, p, sms, s)
+                    : launch_seq_few<64, __nv_bfloat16>(few, mq, mq_few, mk, mv, p, sms, s);
+  return d == 128 ? launch_seq_few<128, __half>(few, mq, mq_few, mk, mv, p, sms, s)
+                  : launch_seq_few<64, __half>(few, mq, mq_few, mk, mv, p, sms, s);
 }
 
 int check_heads(int n_seq, int Tq, int Hq, int Hkv, int d, int dtype) {
@@ -389,7 +414,7 @@ int blasst_packed_fwd(const blasst_packed_args* a) {
   p.cu_k = a->cu_k;
   p.page_size = 1;
   p.n_pages = 1;
-  p.chunk = 128;
+  p.chunk_log2 = 7;
   p.n_seq = a->n_seq;
   p.Tq = a->Tq;
   p.Tk = a->Tk;
@@ -404,7 +429,7 @@ int blasst_packed_fwd(const blasst_packed_args* a) {
   if (!make_map4(&mk, k, a->dtype, {a->d, a->Tk, a->Hkv, 1}, {a->k_st, a->k_sh, 8}, 128, 1) ||
       !make_map4(&mv, v, a->dtype, {a->d, a->Tk, a->Hkv, 1}, {a->v_st, a->v_sh, 8}, 128, 1))
     return BLASST_ECUDA;
-  return run_seq(p, a->q, a->q_st, a->q_sh, a->d, a->scale, a->dtype, mk, mv, a->workspace, sms,
+  return run_seq(p, a->q, a->q_st, a->q_sh, a->d, a->scale, a->dtype, mk, mv, a->Tk, a->workspace, sms,
                  a->stream);
 }
 
@@ -541,7 +566,8 @@ int blasst_paged_fwd(const blasst_paged_args* a) {
   p.table_width = a->table_width;
   p.page_size = a->page_size;
   p.n_pages = a->n_pages;
-  p.chunk = std::min(128, a->page_size & -a->page_size);
+  p.chunk_log2 = 3;
+  while (p.chunk_log2 < 7 && a->page_size % (2 << p.chunk_log2) == 0) ++p.chunk_log2;
   p.n_seq = a->n_seq;
   p.Tq = a->Tq;
   p.Tk = 0;
@@ -551,12 +577,12 @@ int blasst_paged_fwd(const blasst_paged_args* a) {
   p.causal = a->causal ? 1 : 0;
   CUtensorMap mk, mv;
   if (!make_map4(&mk, a->k_pages, a->dtype, {a->d, a->page_size, a->Hkv, a->n_pages},
-                 {a->kp_st, a->kp_sh, a->kp_sp}, p.chunk, 1) ||
+                 {a->kp_st, a->kp_sh, a->kp_sp}, 1 << p.chunk_log2, 1) ||
       !make_map4(&mv, a->v_pages, a->dtype, {a->d, a->page_size, a->Hkv, a->n_pages},
-                 {a->vp_st, a->vp_sh, a->vp_sp}, p.chunk, 1))
+                 {a->vp_st, a->vp_sh, a->vp_sp}, 1 << p.chunk_log2, 1))
     return BLASST_ECUDA;
-  return run_seq(p, a->q, a->q_st, a->q_sh, a->d, a->scale, a->dtype, mk, mv, a->workspace, sms,
-                 a->stream);
+  return run_seq(p, a->q, a->q_st, a->q_sh, a->d, a->scale, a->dtype, mk, mv,
+                 static_cast<long long>(a->table_width) * a->page_size, a->workspace, sms, a->stream);
 }
 
 }  // extern "C"
