@@ -28,9 +28,9 @@
 //              In a kernel of its own (FEW, which takes any item): beside the
 //              others' block loop it made the compiler spill there (3.5 -> 6.2
 //              ms for 32768 prompt tokens of 32 heads).
-// Warps 0-3, 4-7: softmax of stream 0, 1 (thread = row = TMEM lane); warp 8:
-// TMA producer; warp 9: tcgen05 issuer; warp 10: finds the CTA's items and
-// hands the others one record each (11 only fills the warpgroup, which gives
+// Warps 0-3, 4-7: softmax of stream 0, 1 (thread = row = TMEM lane); warps 8
+// and 11: TMA producers of Q and K, and of V; warp 9: tcgen05 issuer; warp 10:
+// finds the CTA's items and hands the others one record each (warps 8-11 give
 // registers to the softmax warps). TMEM: S0, S1 (fp32, 128 columns; P as
 // 16-bit pairs over the first 64 of the same columns once S is in registers),
 // O0, O1.
@@ -69,6 +69,7 @@ struct SeqAttnParams {
   int n_seq, Tq, Tk, Hq, Hkv, g;
   int rt;        // tokens per 128-row tile
   int rt_few;    // tokens per 32 rows (0: a group is larger)
+  int it_tok;    // tokens per item: rt (the kernel for few rows) or 2 rt
   int n_tiles;   // most tiles per KV head (one item per CTA); 0: shared list
   int causal;
   float scale_log2;
@@ -126,27 +127,34 @@ __device__ __forceinline__ SeqSpan seq_span_of(const SeqSpan& q, int l) {
   return r;
 }
 
-template <int D>
+template <int D, bool FEW>
 struct SeqAttnCfg {
   static constexpr int NTHREADS = 384;
   // registers per thread: a softmax thread keeps its 128 scores; 2 x 216 + 72
   // = 3 x 168, what the launch has
   static constexpr int REGS = 168, REGS_SOFT = 216, REGS_REST = 72;
   static constexpr int NSOFT = 256;
-  static constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_ITEM = 10;
+  static constexpr int WARP_K = 8, WARP_MMA = 9, WARP_ITEM = 10, WARP_V = 11;
   static constexpr int BK = 128;
   static constexpr int DBOX = D / 64;
   static constexpr int BOX = 128 * 128;  // [128 rows][64 columns], 16 bits
   static constexpr int TILE = BOX * DBOX;
-  static constexpr int NST = D == 128 ? 5 : 8;  // K / V ring
+  // rings of K and V blocks; the kernel for few rows has one tile of Q, and
+  // what it waits for is memory: more blocks in flight
+  static constexpr int NQ = FEW ? 1 : 2;
+  static constexpr int NK = D == 128 ? 3 : FEW ? 6 : 4;
+  static constexpr int NV = D == 128 ? (FEW ? 3 : 2) : FEW ? 6 : 4;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_KV = 2 * TILE;
-  static constexpr int OFF_BAR = OFF_KV + NST * TILE;
+  static constexpr int OFF_K = NQ * TILE;
+  static constexpr int OFF_V = OFF_K + NK * TILE;
+  static constexpr int OFF_BAR = OFF_V + NV * TILE;
   static constexpr int B_Q = 0;
   static constexpr int B_TAIL = 1;          // V rows of a last block landed (then cleared behind the end)
-  static constexpr int B_KVF = 2;           // [NST]
-  static constexpr int B_KVE = B_KVF + NST; // [NST]
-  static constexpr int B_S = B_KVE + NST;   // [2] S written
+  static constexpr int B_KF = 2;            // [NK]
+  static constexpr int B_KE = B_KF + NK;    // [NK]
+  static constexpr int B_VF = B_KE + NK;    // [NV]
+  static constexpr int B_VE = B_VF + NV;    // [NV]
+  static constexpr int B_S = B_VE + NV;     // [2] S written
   static constexpr int B_P = B_S + 2;       // [2] P written, O rescaled (4 warps)
   static constexpr int B_DONE = B_P + 2;    // every product of the item done
   static constexpr int B_OFREE = B_DONE + 1;  // O read (8 warps)
@@ -155,7 +163,7 @@ struct SeqAttnCfg {
   static constexpr int B_DRAIN = B_X + 1;
   static constexpr int NITEM = 2;
   static constexpr int B_IF = B_DRAIN + 1;   // [NITEM] item record written
-  static constexpr int B_IE = B_IF + NITEM;  // [NITEM] read (loader, issuer, 8 softmax warps)
+  static constexpr int B_IE = B_IF + NITEM;  // [NITEM] read (2 loaders, issuer, 8 softmax warps)
   static constexpr int NBAR = B_IE + NITEM;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   // misc words: [0] tmem base, [1] abort, [3] always 0
@@ -185,10 +193,10 @@ struct SeqItem {
   bool one;  // one tile: both streams share its rows
 };
 
-__device__ __forceinline__ SeqItem seq_item(const SeqSpan& q, int causal, int rt, int t) {
+__device__ __forceinline__ SeqItem seq_item(const SeqSpan& q, int causal, int rt, int it_tok, int t) {
   SeqItem it;
-  it.tok0 = t * 2 * rt;
-  it.ntok = min(2 * rt, q.qlen - it.tok0);
+  it.tok0 = t * it_tok;
+  it.ntok = min(it_tok, q.qlen - it.tok0);
   it.one = it.ntok <= rt;
   it.nblk = seq_blocks(q, causal, it.tok0 + it.ntok - 1);
   it.nblk0 = it.one ? it.nblk : seq_blocks(q, causal, it.tok0 + rt - 1);
@@ -196,13 +204,20 @@ __device__ __forceinline__ SeqItem seq_item(const SeqSpan& q, int causal, int rt
   return it;
 }
 
-__device__ __forceinline__ long long seq_cost(const SeqSpan& q, int causal, int rt) {
+__device__ __forceinline__ long long seq_cost(const SeqSpan& q, int causal, int rt, int it_tok) {
   long long c = 0;
   for (int t = 0; t < q.tiles; ++t) {
-    const SeqItem it = seq_item(q, causal, rt, t);
+    const SeqItem it = seq_item(q, causal, rt, it_tok, t);
     c += kSeqItemCost + static_cast<long long>(it.nblk) * it.unit;
   }
   return c;
+}
+
+// a / b of non-negative numbers; 64-bit division only where it is needed (it
+// took a fifth of a short call's kernel).
+__device__ __forceinline__ long long seq_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
 // Blocks [b0, b1) of an item that starts at `at` in the list and fall into
@@ -210,7 +225,7 @@ __device__ __forceinline__ long long seq_cost(const SeqSpan& q, int causal, int 
 __device__ __forceinline__ int seq_first_block(long long at, const SeqItem& it, long long lo) {
   if (lo <= at) return 0;
   const long long x = lo - at - kSeqItemCost;
-  const long long b = x <= 0 ? 1 : (x + it.unit - 1) / it.unit;
+  const long long b = x <= 0 ? 1 : (x + it.unit - 1) >> (it.unit - 1);  // unit is 1 or 2
   return static_cast<int>(b < 1 ? 1 : (b > it.nblk ? it.nblk : b));
 }
 
@@ -248,46 +263,39 @@ struct SeqType<__half> {
   static constexpr uint32_t kFormat = 0;
 };
 
-// Few rows: a lane's sums of both streams over half of the columns, weighted,
-// to shared memory; a weight of 0 takes nothing (the sum may never have been
-// written).
+// Few rows: a lane's sums of both streams over D / 4 columns from `col` on,
+// weighted, to shared memory; a weight of 0 takes nothing (the sum may never
+// have been written).
 template <int D>
-__device__ __forceinline__ void seq_few_put(uint32_t o_tm, float* x, float w0, float w1) {
-#pragma unroll 1
-  for (int c = 0; c < D / 64; ++c) {
-    uint32_t r0[32], r1[32];
-    ptx::tmem_ld32(o_tm + 32 * c, r0);
-    ptx::tmem_ld32(o_tm + D + 32 * c, r1);
-    ptx::tmem_wait_ld();
+__device__ __forceinline__ void seq_few_put(uint32_t o_tm, int col, float* x, float w0, float w1) {
+  uint32_t r0[32], r1[32];
+  const int skip = col & 31;  // d = 64: half of a load
+  ptx::tmem_ld32(o_tm + (col & ~31), r0);
+  ptx::tmem_ld32(o_tm + D + (col & ~31), r1);
+  ptx::tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float a = w0 == 0.0f ? 0.0f : w0 * __uint_as_float(r0[j]);
-      x[(32 * c + j) * 32] = w1 == 0.0f ? a : fmaf(w1, __uint_as_float(r1[j]), a);
-    }
+  for (int j = 0; j < 32; ++j) {
+    if (j < skip || j >= skip + D / 4) continue;
+    const float a = w0 == 0.0f ? 0.0f : w0 * __uint_as_float(r0[j]);
+    x[(j - skip) * 32] = w1 == 0.0f ? a : fmaf(w1, __uint_as_float(r1[j]), a);
   }
 }
 
-// Adds up the four quarters' sums of a row over D / 8 columns; to `part`
+// Adds up the four quarters' sums of a row over D / 16 columns; to `part`
 // (fp32) if there is one, else to `o`.
 template <int D, typename T>
 __device__ __forceinline__ void seq_few_take(const float* x, T* o, float* part) {
-  constexpr int Q = D / 2 * 32;
-#pragma unroll 1
-  for (int c = 0; c < D / 64; ++c) {
-    float v[8];
+  constexpr int Q = D / 4 * 32;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float* y = x + (8 * c + j) * 32;
+  for (int c = 0; c < D / 64; ++c) {
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float* y = x + (4 * c + j) * 32;
       v[j] = (y[0] + y[Q]) + (y[2 * Q] + y[3 * Q]);
     }
-    if (part) {
-      reinterpret_cast<float4*>(part + 8 * c)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(part + 8 * c)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      *reinterpret_cast<uint4*>(o + 8 * c) =
-          make_uint4(seq_pack2<T>(v[0], v[1]), seq_pack2<T>(v[2], v[3]), seq_pack2<T>(v[4], v[5]),
-                     seq_pack2<T>(v[6], v[7]));
-    }
+    if (part) *reinterpret_cast<float4*>(part + 4 * c) = make_float4(v[0], v[1], v[2], v[3]);
+    else *reinterpret_cast<uint2*>(o + 4 * c) = make_uint2(seq_pack2<T>(v[0], v[1]), seq_pack2<T>(v[2], v[3]));
   }
 }
 
@@ -297,7 +305,7 @@ __global__ void __launch_bounds__(384, 1)
                            const __grid_constant__ CUtensorMap tmQFew,
                            const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const SeqAttnParams p) {
-  using C = SeqAttnCfg<D>;
+  using C = SeqAttnCfg<D, FEW>;
   constexpr uint32_t IDESC_S = ptx::idesc_f32acc(SeqType<T>::kFormat, 128, 128, false);
   constexpr uint32_t IDESC_PV = ptx::idesc_f32acc(SeqType<T>::kFormat, 128, D, true);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -319,14 +327,11 @@ __global__ void __launch_bounds__(384, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NITEM; ++i) {
       ptx::mbar_init(bar(C::B_IF + i), 1);
-      ptx::mbar_init(bar(C::B_IE + i), 10);
+      ptx::mbar_init(bar(C::B_IE + i), 11);
     }
     ptx::mbar_init(bar(C::B_Q), 1);
     ptx::mbar_init(bar(C::B_TAIL), 1);
-    for (int i = 0; i < C::NST; ++i) {
-      ptx::mbar_init(bar(C::B_KVF + i), 1);
-      ptx::mbar_init(bar(C::B_KVE + i), 1);
-    }
+    for (int i = 0; i < 2 * (C::NK + C::NV); ++i) ptx::mbar_init(bar(C::B_KF + i), 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bar(C::B_S + i), 1);
       ptx::mbar_init(bar(C::B_P + i), 4);
@@ -383,7 +388,7 @@ __global__ void __launch_bounds__(384, 1)
         min(static_cast<long long>(p.table_width) * p.page_size, 0x7fffff00ll));
     auto span = [&](int s) -> SeqSpan {
       if (s < 0 || s >= p.n_seq) return SeqSpan{};
-      return seq_span(p.cu_q, p.cu_k, p.kv_lens, kv_cap, p.Tq, p.Tk, 2 * p.rt, s, p.err);
+      return seq_span(p.cu_q, p.cu_k, p.kv_lens, kv_cap, p.Tq, p.Tk, p.it_tok, s, p.err);
     };
     int n = 0;
     auto put = [&](int s, const SeqSpan& q, int h, const SeqItem& it, int b0, int b1) -> bool {
@@ -436,7 +441,7 @@ __global__ void __launch_bounds__(384, 1)
           const int l = __ffs(hit) - 1;
           const int end = before + __shfl_sync(0xffffffffu, upto, l);
           const SeqSpan q = seq_span_of(mine, l);
-          const SeqItem it = seq_item(q, p.causal, p.rt, end - 1 - want);
+          const SeqItem it = seq_item(q, p.causal, p.rt, p.it_tok, end - 1 - want);
           ok = put(s0 - l, q, h, it, 0, it.nblk);
           found = true;
         }
@@ -462,13 +467,13 @@ __global__ void __launch_bounds__(384, 1)
       long long total = 0, own = 0;
       for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
         load_chunk(s0);
-        own = seq_cost(mine, p.causal, p.rt) * p.Hkv;
+        own = seq_cost(mine, p.causal, p.rt, p.it_tok) * p.Hkv;
         long long c = own;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
         total += c;
       }
-      const long long share = (total + gridDim.x - 1) / gridDim.x;
+      const long long share = seq_div(total + gridDim.x - 1, gridDim.x);
       const long long range = share < kSeqMinRange ? kSeqMinRange : share;
       const long long lo = range * blockIdx.x;
       const long long hi = lo + range < total ? lo + range : total;
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__(384, 1)
       for (int s0 = 0; s0 < p.n_seq && !found && live && lo < total; s0 += 32) {
         if (s0 != chunk) {
           load_chunk(s0);
-          own = seq_cost(mine, p.causal, p.rt) * p.Hkv;
+          own = seq_cost(mine, p.causal, p.rt, p.it_tok) * p.Hkv;
         }
         long long upto = own;
 #pragma unroll
@@ -490,9 +495,9 @@ __global__ void __launch_bounds__(384, 1)
         if (hit) {
           const int l = __ffs(hit) - 1;
           at += __shfl_sync(0xffffffffu, upto - own, l);
-          const long long per_head = __shfl_sync(0xffffffffu, own, l) / p.Hkv;
+          const long long per_head = seq_div(__shfl_sync(0xffffffffu, own, l), p.Hkv);
           s = s0 + l;
-          h = static_cast<int>((lo - at) / per_head);
+          h = static_cast<int>(seq_div(lo - at, per_head));
           at += h * per_head;
           found = true;
         } else {
@@ -502,7 +507,7 @@ __global__ void __launch_bounds__(384, 1)
       if (found) {
         SeqSpan q = span_of(s);
         while (at < hi && ok) {
-          const SeqItem it = seq_item(q, p.causal, p.rt, t);
+          const SeqItem it = seq_item(q, p.causal, p.rt, p.it_tok, t);
           const long long end = at + kSeqItemCost + static_cast<long long>(it.nblk) * it.unit;
           if (end > lo) {
             const int b0 = it.nblk ? seq_first_block(at, it, lo) : 0;
@@ -515,7 +520,7 @@ __global__ void __launch_bounds__(384, 1)
                 p.part_desc[2 * blockIdx.x] =
                     make_int4(q.q0 + it.tok0, it.ntok, h, it.one ? 1 : 0);
                 p.part_desc[2 * blockIdx.x + 1] =
-                    make_int4(static_cast<int>((end - it.unit) / range), 0, 0, 0);
+                    make_int4(static_cast<int>(seq_div(end - it.unit, range)), 0, 0, 0);
               }
               ok = put(s, q, h, it, b0, b1);
             }
@@ -541,39 +546,67 @@ __global__ void __launch_bounds__(384, 1)
       ok = put(-1, q, 0, it, 0, 0);  // the end
     }
     if (!ok && lane == 0) fail();
-  } else if (warp == C::WARP_LOAD) {
-    // ======================= TMA producer ==================================
+  } else if (warp == C::WARP_K || warp == C::WARP_V) {
+    // ======================= TMA producers =================================
+    // One warp for K (and Q), one for V. Their own time per block counts: with
+    // one warp for both, a table entry read per block and divisions in the
+    // loop, a step of single tokens was bound by it.
+    const bool is_v = warp == C::WARP_V;
+    const CUtensorMap* tm = is_v ? &tmV : &tmK;
+    const uint32_t depth = is_v ? C::NV : C::NK;
+    const int b_full = is_v ? C::B_VF : C::B_KF, b_empty = is_v ? C::B_VE : C::B_KE;
+    const int ring_off = is_v ? C::OFF_V : C::OFF_K;
     if (lane == 0) {
-      ptx::prefetch_tmap(&tmQ);
-      ptx::prefetch_tmap(&tmK);
-      ptx::prefetch_tmap(&tmV);
+      ptx::prefetch_tmap(tm);
+      if (!is_v) ptx::prefetch_tmap(FEW ? &tmQFew : &tmQ);
     }
-    // (no divisions in the loop over loads: this warp's own time per load is
-    // what a step of single tokens was bound by, 1.03 ms -> see below)
     const int chunk = 1 << p.chunk_log2;
     const int nch_log2 = 7 - p.chunk_log2, nch = 1 << nch_log2;
     const int q_box_rows = p.g * p.rt;
     // Places in the cache (page, row in it) are looked up a group of 32 chunks
-    // (one per lane) at a time, one group ahead of their use: the groups
-    // before, at and behind the newest K block (V follows one block later).
+    // (one per lane) at a time, one group ahead of their use.
     const int group_log2 = 5 - nch_log2;  // blocks of a group
-    int2 at_before = make_int2(0, 0), at_now = at_before, at_next = at_before;
+    int2 at_now = make_int2(0, 0), at_next = at_now;
     int group = -1;
-    uint32_t ring = 0;   // loads issued
+    uint32_t ring = 0;            // loads issued
     uint32_t slot = 0, turn = 0;  // of the ring; turn: parity of the slot's phase
-    uint32_t tails = 0;  // cleared last blocks
+    uint32_t tails = 0;           // cleared last blocks
     bool ok = true;
     bool last_tail = false;
     int q_loads = 0;
     bool few_before = false;
     SeqRecord it;
+    auto load_q = [&](int n) -> bool {
+      // once the item before has finished with it (the first K blocks do not
+      // wait for that); few rows leave their sums in Q's place
+      if (n > 0 && !ptx::mbar_wait(bar(C::B_DONE), (n - 1) & 1, abort_flag, p.timeout_ns)) return false;
+      // (only behind the wait above is the phase before known to be over)
+      if (FEW && few_before &&
+          !ptx::mbar_wait(bar(C::B_OFREE), (n - 1) & 1, abort_flag, p.timeout_ns))
+        return false;
+      const bool few = FEW && it.few();
+      const int parts = few ? 4 : it.one() ? 1 : 2;
+      ptx::mbar_arrive_expect_tx(bar(C::B_Q),
+                                 parts * C::DBOX * (few ? p.g * p.rt_few : q_box_rows) * 128);
+      for (int i = 0; i < parts; ++i)
+#pragma unroll
+        for (int x = 0; x < C::DBOX; ++x) {
+          if (few)
+            ptx::tma_load_4d(sb + C::OFF_Q + x * C::BOX + i * 32 * 128, &tmQFew, x * 64, 0, it.qtok,
+                             it.hk, bar(C::B_Q));
+          else
+            ptx::tma_load_4d(sb + C::OFF_Q + i * C::TILE + x * C::BOX, &tmQ, x * 64, 0,
+                             it.qtok + i * p.rt, it.hk, bar(C::B_Q));
+        }
+      q_loads = n + 1;
+      return true;
+    };
     for (int n = 0; ok; ++n) {
       ok = __all_sync(0xffffffffu, next_item(n, it)) != 0;
       if (!ok) break;
       if (lane == 0) item_read(n);
       if (it.seq < 0) break;
       const int nb = it.nb;
-      const int nload = 2 * nb;
       auto read_group = [&](int gr) -> int2 {
         const long long key = (static_cast<long long>(gr) * 32 + lane) << p.chunk_log2;
         if (key >= it.kvlen) return make_int2(p.n_pages, 0);
@@ -586,56 +619,14 @@ __global__ void __launch_bounds__(384, 1)
         at_now = read_group(group);
         at_next = read_group(group + 1);
       }
-      const int q_at = n == 0 ? 0 : (nb >= 2 ? 3 : min(1, nload));
-      for (int r = 0; r <= nload && ok; ++r) {
-        if (r == q_at) {
-          // Q, once the item before has finished with it (its first K and V
-          // do not wait for that); few rows leave their sums in Q's place
-          if (lane == 0) {
-            if (n > 0)
-              ok = ptx::mbar_wait(bar(C::B_DONE), (n - 1) & 1, abort_flag, p.timeout_ns);
-            // (only behind the wait above is the phase before known to be over)
-            if (FEW && ok && few_before)
-              ok = ptx::mbar_wait(bar(C::B_OFREE), (n - 1) & 1, abort_flag, p.timeout_ns);
-            if (FEW && ok && it.few()) {
-              ptx::mbar_arrive_expect_tx(bar(C::B_Q), 4 * C::DBOX * p.g * p.rt_few * 128);
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int x = 0; x < C::DBOX; ++x)
-                  ptx::tma_load_4d(sb + C::OFF_Q + x * C::BOX + i * 32 * 128, &tmQFew, x * 64, 0,
-                                   it.qtok, it.hk, bar(C::B_Q));
-              q_loads = n + 1;
-            } else if (ok) {
-              const int tiles = it.one() ? 1 : 2;
-              ptx::mbar_arrive_expect_tx(bar(C::B_Q), tiles * C::DBOX * q_box_rows * 128);
-              for (int i = 0; i < tiles; ++i)
-#pragma unroll
-                for (int x = 0; x < C::DBOX; ++x)
-                  ptx::tma_load_4d(sb + C::OFF_Q + i * C::TILE + x * C::BOX, &tmQ, x * 64, 0,
-                                   it.qtok + i * p.rt, it.hk, bar(C::B_Q));
-              q_loads = n + 1;
-            }
-          }
+      const int q_at = n == 0 ? 0 : min(nb, 2);
+      for (int b = 0; b <= nb && ok; ++b) {
+        if (!is_v && b == q_at) {
+          if (lane == 0) ok = load_q(n);
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
           few_before = it.few();
         }
-        if (r == nload || !ok) break;
-        // the order in which the issuer takes the blocks
-        bool is_v;
-        int b;
-        if (!it.one()) {
-          is_v = r & 1;
-          b = r >> 1;
-        } else if (r < 2 && r < nb) {
-          is_v = false;
-          b = r;
-        } else if (r == nload - 1) {
-          is_v = true;
-          b = nb - 1;
-        } else {
-          is_v = (r & 1) == 0;
-          b = is_v ? (r - 2) >> 1 : (r + 1) >> 1;
-        }
+        if (b == nb || !ok) break;
         const int key0 = (it.b0 + b) * C::BK;
         const int valid = min(C::BK, it.kvlen - key0);
         // this lane's piece of the block
@@ -643,46 +634,39 @@ __global__ void __launch_bounds__(384, 1)
         const bool mine = lane < nch && (lane << p.chunk_log2) < valid;
         if (p.table) {
           const int block = it.b0 + b;
-          if ((block >> group_log2) > group) {  // K moves on
+          if ((block >> group_log2) > group) {
             ++group;
-            at_before = at_now;
             at_now = at_next;
             at_next = read_group(group + 1);
           }
-          const bool now = (block >> group_log2) == group;
           const int from = ((block & ((1 << group_log2) - 1)) << nch_log2) + (lane & (nch - 1));
-          page = __shfl_sync(0xffffffffu, now ? at_now.x : at_before.x, from);
-          row = __shfl_sync(0xffffffffu, now ? at_now.y : at_before.y, from);
+          page = __shfl_sync(0xffffffffu, at_now.x, from);
+          row = __shfl_sync(0xffffffffu, at_now.y, from);
           if (mine && static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages)) {
             seq_record_error(p.err, BLASST_EINDEX);
             page = p.n_pages;  // outside the map: zeros
           }
         }
-        const uint32_t st = slot;
-        const uint32_t full = bar(C::B_KVF + st);
+        const uint32_t full = bar(b_full + slot);
         const bool tail = is_v && valid < C::BK;
         const uint32_t fb = tail ? bar(C::B_TAIL) : full;
         if (lane == 0) {
-          if (ring >= C::NST)
-            ok = ptx::mbar_wait(bar(C::B_KVE + st), turn ^ 1u, abort_flag, p.timeout_ns);
+          if (ring >= depth)
+            ok = ptx::mbar_wait(bar(b_empty + slot), turn ^ 1u, abort_flag, p.timeout_ns);
           if (ok)
             ptx::mbar_arrive_expect_tx(fb, ((valid + chunk - 1) >> p.chunk_log2 << p.chunk_log2) *
                                                (128 * C::DBOX));
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok) break;
-        const uint32_t dst = sb + C::OFF_KV + st * C::TILE;
+        const int dst = ring_off + static_cast<int>(slot) * C::TILE;
         if (mine) {
-          const CUtensorMap* tm = is_v ? &tmV : &tmK;
 #pragma unroll
           for (int x = 0; x < C::DBOX; ++x)
-            ptx::tma_load_4d(dst + x * C::BOX + (lane << p.chunk_log2) * 128, tm, x * 64, row, it.hk, page, fb);
+            ptx::tma_load_4d(sb + dst + x * C::BOX + (lane << p.chunk_log2) * 128, tm, x * 64, row,
+                             it.hk, page, fb);
         }
         ++ring;
-        if (++slot == C::NST) {
-          slot = 0;
-          turn ^= 1u;
-        }
         last_tail = tail;
         if (tail) {
           // Rows behind the sequence's end (a neighbour's, a page's leftovers,
@@ -695,12 +679,15 @@ __global__ void __launch_bounds__(384, 1)
           for (int i = valid * 8 + lane; i < C::BK * 8; i += 32)
 #pragma unroll
             for (int x = 0; x < C::DBOX; ++x)
-              *reinterpret_cast<uint4*>(smem + C::OFF_KV + st * C::TILE + x * C::BOX + i * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(smem + dst + x * C::BOX + i * 16) = make_uint4(0u, 0u, 0u, 0u);
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(full);
           last_tail = false;
+        }
+        if (++slot == depth) {
+          slot = 0;
+          turn ^= 1u;
         }
       }
     }
@@ -708,9 +695,9 @@ __global__ void __launch_bounds__(384, 1)
       fail();
       // copies in flight land before the CTA exits (1 ms each is ample)
       const uint64_t drain_ns = p.timeout_ns < 1000000ull ? p.timeout_ns : 1000000ull;
-      for (uint32_t k = ring < C::NST ? 0 : ring - C::NST; k < ring; ++k)
+      for (uint32_t k = ring < depth ? 0 : ring - depth; k < ring; ++k)
         if (!(last_tail && k + 1 == ring))
-          ptx::mbar_wait(bar(C::B_KVF + k % C::NST), (k / C::NST) & 1, &misc[3], drain_ns);
+          ptx::mbar_wait(bar(b_full + k % depth), (k / depth) & 1, &misc[3], drain_ns);
       if (last_tail) ptx::mbar_wait(bar(C::B_TAIL), (tails - 1) & 1, &misc[3], drain_ns);
       if (q_loads > 0) ptx::mbar_wait(bar(C::B_Q), (q_loads - 1) & 1, &misc[3], drain_ns);
     }
@@ -719,9 +706,9 @@ __global__ void __launch_bounds__(384, 1)
     if (lane == 0) {
       bool ok = true;
       const uint64_t q_desc = ptx::sw128_desc(sb + C::OFF_Q, 16, 1024);
-      const uint64_t k_desc = ptx::sw128_desc(sb + C::OFF_KV, 16, 1024);
-      const uint64_t v_desc = ptx::sw128_desc(sb + C::OFF_KV, C::BOX, 1024);
-      uint32_t ring0 = 0;                 // ring position of the item's first load
+      const uint64_t k_desc = ptx::sw128_desc(sb + C::OFF_K, 16, 1024);
+      const uint64_t v_desc = ptx::sw128_desc(sb + C::OFF_V, C::BOX, 1024);
+      uint32_t ring0 = 0;                 // ring position of the item's first blocks
       uint32_t steps[2] = {0, 0};         // blocks done per stream (P phases)
       SeqRecord it;
       for (int n = 0; ok; ++n) {
@@ -736,9 +723,9 @@ __global__ void __launch_bounds__(384, 1)
         if (!ok) break;
         auto issue_s = [&](int st, int i) -> bool {
           const int b = one ? 2 * i + st : i;
-          const uint32_t k = ring0 + (one ? (b < 2 ? b : 2 * b - 1) : 2 * b);
-          const uint32_t slot = k % C::NST;
-          if (!ptx::mbar_wait(bar(C::B_KVF + slot), (k / C::NST) & 1, abort_flag, p.timeout_ns))
+          const uint32_t k = ring0 + b;
+          const uint32_t slot = k % C::NK;
+          if (!ptx::mbar_wait(bar(C::B_KF + slot), (k / C::NK) & 1, abort_flag, p.timeout_ns))
             return false;
           ptx::tc_fence_after();
           const uint64_t qd =
@@ -750,18 +737,17 @@ __global__ void __launch_bounds__(384, 1)
             ptx::mma_ss(tmem + C::S_COL + st * 128, qd + o, kd + o, IDESC_S, kk > 0 ? 1u : 0u);
           }
           ptx::mma_commit(bar(C::B_S + st));
-          if (one || st == 1) ptx::mma_commit(bar(C::B_KVE + slot));
+          if (one || st == 1) ptx::mma_commit(bar(C::B_KE + slot));
           return true;
         };
         auto issue_pv = [&](int st, int i) -> bool {
           const int b = one ? 2 * i + st : i;
-          const uint32_t k =
-              ring0 + (one ? (b == nb - 1 ? 2 * nb - 1 : 2 * b + 2) : 2 * b + 1);
-          const uint32_t slot = k % C::NST;
+          const uint32_t k = ring0 + b;
+          const uint32_t slot = k % C::NV;
           if (!ptx::mbar_wait(bar(C::B_P + st), steps[st] & 1, abort_flag, p.timeout_ns))
             return false;
           ++steps[st];
-          if (!ptx::mbar_wait(bar(C::B_KVF + slot), (k / C::NST) & 1, abort_flag, p.timeout_ns))
+          if (!ptx::mbar_wait(bar(C::B_VF + slot), (k / C::NV) & 1, abort_flag, p.timeout_ns))
             return false;
           ptx::tc_fence_after();
           const uint64_t vd = v_desc + static_cast<uint64_t>(slot * (C::TILE >> 4));
@@ -772,7 +758,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int kk = 1; kk < C::BK / 16; ++kk)
             ptx::mma_ts(o_tm, p_tm + kk * 8, vd + static_cast<uint64_t>(kk * (2048 >> 4)), IDESC_PV,
                         1u);
-          if (one || st == 1) ptx::mma_commit(bar(C::B_KVE + slot));
+          if (one || st == 1) ptx::mma_commit(bar(C::B_VE + slot));
           return true;
         };
         for (int st = 0; st < 2 && ok; ++st)
@@ -786,7 +772,7 @@ __global__ void __launch_bounds__(384, 1)
             if (ok && i + 1 < cnt[st]) ok = issue_s(st, i + 1);
           }
         ptx::mma_commit(bar(C::B_DONE));
-        ring0 += 2 * nb;
+        ring0 += nb;
       }
       if (!ok) fail();
       // every product has completed before TMEM is freed
@@ -826,7 +812,7 @@ __global__ void __launch_bounds__(384, 1)
         ptx::tmem_st32(o_tm + 32 * c, r);
       }
     };
-    uint32_t fews = 0;  // items of few rows done
+    uint32_t meets = 0;  // B_X phases
     SeqRecord it;
     for (int n = 0; ok; ++n) {
       ok = __all_sync(0xffffffffu, next_item(n, it)) != 0;
@@ -1009,21 +995,33 @@ __global__ void __launch_bounds__(384, 1)
       const bool second = one && it.nb > 1;
       if (few) {
         // each quarter's sums, [quarter][column][row] fp32, this warpgroup's
-        // half of the columns; then every warp adds up a quarter of those
-        constexpr int HALF = D / 2;
-        float* x = reinterpret_cast<float*>(smem + C::OFF_Q) + st * 4 * HALF * 32 + lane;
-        seq_few_put<D>(tmem + lane_base + C::O_COL + st * HALF, x + quad * HALF * 32,
-                       it.nb > 0 && l != 0.0f ? w0 * inv : 0.0f, second && l != 0.0f ? w1 * inv : 0.0f);
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(C::B_X));
-        ok = lane0_wait(bar(C::B_X), fews & 1);
-        ++fews;
-        if (!ok) break;
-        if (exists) {
-          const int col = st * HALF + quad * (HALF / 4);
-          seq_few_take<D, T>(x + quad * (HALF / 4) * 32, static_cast<T*>(p.o) + tok_row * D + col,
-                             whole ? nullptr : p.part_o + (static_cast<size_t>(slot) * 256 + lane) * D + col);
+        // half of the columns in two rounds; every warp adds up a quarter of
+        // a round's columns
+        constexpr int CR = D / 4;
+        float* x = reinterpret_cast<float*>(smem + C::OFF_Q) + st * 4 * CR * 32 + lane;
+        const float f0 = it.nb > 0 && l != 0.0f ? w0 * inv : 0.0f;
+        const float f1 = second && l != 0.0f ? w1 * inv : 0.0f;
+        auto meet = [&]() -> bool {  // all 8 warps
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(C::B_X));
+          return lane0_wait(bar(C::B_X), meets++ & 1);
+        };
+#pragma unroll 1
+        for (int round = 0; round < 2 && ok; ++round) {
+          if (round > 0) ok = meet();
+          if (!ok) break;
+          const int col = st * (D / 2) + round * CR;
+          seq_few_put<D>(tmem + lane_base + C::O_COL, col, x + quad * CR * 32, f0, f1);
+          ok = meet();
+          if (ok && exists)
+            seq_few_take<D, T>(x + quad * (CR / 4) * 32, static_cast<T*>(p.o) + tok_row * D + col + quad * (CR / 4),
+                               whole ? nullptr
+                                     : p.part_o + (static_cast<size_t>(slot) * 256 + lane) * D + col +
+                                           quad * (CR / 4));
         }
+        // (the copies that refill Q's place follow these reads and writes)
+        ptx::fence_proxy_async_smem();
+        if (!ok) break;
       } else if (active) {
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; ++c) {

@@ -80,7 +80,7 @@ int check_regs(K kernel, int regs, int& known) {
 template <int D, typename T, bool FEW>
 int launch_seq(const CUtensorMap& mq, const CUtensorMap& mq_few, const CUtensorMap& mk,
                const CUtensorMap& mv, const blasst::SeqAttnParams& p, int sms, cudaStream_t stream) {
-  using C = blasst::SeqAttnCfg<D>;
+  using C = blasst::SeqAttnCfg<D, FEW>;
   auto kernel = blasst::blasst_seq_attn_kernel<D, T, FEW>;
   static int regs = 0;  // of this instantiation
   if (const int rc = check_regs(kernel, C::REGS, regs)) return rc;
@@ -124,7 +124,11 @@ int run_seq(blasst::SeqAttnParams& p, const void* q, long long q_st, long long q
   // then shares K and V in L2), or if no sequence can have many keys (nothing
   // worth cutting, and no second kernel). Fewer tiles, or mostly single tokens:
   // the shared list, which cuts long rows of key blocks between SMs.
-  const long long full = static_cast<long long>(p.Tq) / (2 * p.rt);
+  // the kernel for few rows when the sequences have up to 32 rows on average
+  p.rt_few = p.g <= 32 ? 32 / p.g : 0;
+  const bool few = p.rt_few > 0 && static_cast<long long>(p.Tq) * p.g <= 32ll * p.n_seq;
+  p.it_tok = few ? p.rt : 2 * p.rt;
+  const long long full = static_cast<long long>(p.Tq) / p.it_tok;
   const long long tiles = std::min<long long>(p.Tq, full + p.n_seq);
   const bool single = full * p.Hkv >= 8ll * sms || most_keys <= kSeqFewKeys;
   p.n_tiles = single && tiles * p.Hkv < 0x7fffffffll ? static_cast<int>(tiles) : 0;
@@ -135,15 +139,12 @@ int run_seq(blasst::SeqAttnParams& p, const void* q, long long q_st, long long q
   const double sc = scale > 0.0f ? static_cast<double>(scale) : 1.0 / std::sqrt(static_cast<double>(d));
   p.scale_log2 = static_cast<float>(sc * 1.4426950408889634);
   p.timeout_ns = kTimeoutNs;
-  p.rt_few = p.g <= 32 ? 32 / p.g : 0;
   CUtensorMap mq, mq_few;
   if (!make_map4(&mq, q, dtype, {d, p.g, p.Tq, p.Hkv}, {q_sh, q_st, q_sh * p.g}, p.g, p.rt) ||
       !make_map4(&mq_few, q, dtype, {d, p.g, p.Tq, p.Hkv}, {q_sh, q_st, q_sh * p.g}, p.g,
                  std::max(1, p.rt_few)))
     return BLASST_ECUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // the kernel for few rows when the sequences have up to 32 rows on average
-  const bool few = p.rt_few > 0 && static_cast<long long>(p.Tq) * p.g <= 32ll * p.n_seq;
   if (dtype == BLASST_BF16)
     return d == 128 ? launch_seq_few<128, __nv_bfloat16>(few, mq, mq_few, mk, mv, p, sms, s)
                     : launch_seq_few<64, __nv_bfloat16>(few, mq, mq_few, mk, mv, p, sms, s);
