@@ -132,7 +132,7 @@ struct SeqAttnCfg {
   static constexpr int NTHREADS = 384;
   // registers per thread: a softmax thread keeps its 128 scores; 2 x 216 + 72
   // = 3 x 168, what the launch has
-  static constexpr int REGS = 168, REGS_SOFT = 216, REGS_REST = 72;
+  static constexpr int REGS = 168, REGS_SOFT = 200, REGS_REST = 104;
   static constexpr int NSOFT = 256;
   static constexpr int WARP_K = 8, WARP_MMA = 9, WARP_ITEM = 10, WARP_V = 11;
   static constexpr int BK = 128;
@@ -155,8 +155,9 @@ struct SeqAttnCfg {
   static constexpr int B_VF = B_KE + NK;    // [NV]
   static constexpr int B_VE = B_VF + NV;    // [NV]
   static constexpr int B_S = B_VE + NV;     // [2] S written
-  static constexpr int B_P = B_S + 2;       // [2] P written, O rescaled (4 warps)
-  static constexpr int B_DONE = B_P + 2;    // every product of the item done
+  static constexpr int B_P = B_S + 2;       // [2][2] half of P written, O rescaled (4 warps)
+  static constexpr int B_PV = B_P + 4;      // [2] P V of the first half done
+  static constexpr int B_DONE = B_PV + 2;   // every product of the item done
   static constexpr int B_OFREE = B_DONE + 1;  // O read (8 warps)
   static constexpr int B_ML = B_OFREE + 1;  // (m, l) of both streams of a one-tile item (8 warps)
   static constexpr int B_X = B_ML + 1;      // few rows: sums in shared memory (8 warps)
@@ -334,7 +335,9 @@ __global__ void __launch_bounds__(384, 1)
     for (int i = 0; i < 2 * (C::NK + C::NV); ++i) ptx::mbar_init(bar(C::B_KF + i), 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bar(C::B_S + i), 1);
-      ptx::mbar_init(bar(C::B_P + i), 4);
+      ptx::mbar_init(bar(C::B_P + 2 * i), 4);
+      ptx::mbar_init(bar(C::B_P + 2 * i + 1), 4);
+      ptx::mbar_init(bar(C::B_PV + i), 1);
     }
     ptx::mbar_init(bar(C::B_DONE), 1);
     ptx::mbar_init(bar(C::B_OFREE), 8);
@@ -725,7 +728,10 @@ __global__ void __launch_bounds__(384, 1)
           const int b = one ? 2 * i + st : i;
           const uint32_t k = ring0 + b;
           const uint32_t slot = k % C::NK;
-          if (!ptx::mbar_wait(bar(C::B_KF + slot), (k / C::NK) & 1, abort_flag, p.timeout_ns))
+          // (a block both streams use is waited for once: every look at a barrier
+          // costs this thread as much as a product)
+          if ((one || st == 0 || i >= cnt[0]) &&
+              !ptx::mbar_wait(bar(C::B_KF + slot), (k / C::NK) & 1, abort_flag, p.timeout_ns))
             return false;
           ptx::tc_fence_after();
           const uint64_t qd =
@@ -744,20 +750,26 @@ __global__ void __launch_bounds__(384, 1)
           const int b = one ? 2 * i + st : i;
           const uint32_t k = ring0 + b;
           const uint32_t slot = k % C::NV;
-          if (!ptx::mbar_wait(bar(C::B_P + st), steps[st] & 1, abort_flag, p.timeout_ns))
+          // the first half of the keys as soon as its P is there
+          const uint32_t phase = steps[st]++ & 1;
+          if ((one || st == 0 || i >= cnt[0]) &&
+              !ptx::mbar_wait(bar(C::B_VF + slot), (k / C::NV) & 1, abort_flag, p.timeout_ns))
             return false;
-          ++steps[st];
-          if (!ptx::mbar_wait(bar(C::B_VF + slot), (k / C::NV) & 1, abort_flag, p.timeout_ns))
-            return false;
+          if (!ptx::mbar_wait(bar(C::B_P + 2 * st), phase, abort_flag, p.timeout_ns)) return false;
           ptx::tc_fence_after();
           const uint64_t vd = v_desc + static_cast<uint64_t>(slot * (C::TILE >> 4));
           const uint32_t o_tm = tmem + C::O_COL + st * D;
           const uint32_t p_tm = tmem + C::S_COL + st * 128;
           ptx::mma_ts(o_tm, p_tm, vd, IDESC_PV, i > 0 ? 1u : 0u);
 #pragma unroll
-          for (int kk = 1; kk < C::BK / 16; ++kk)
-            ptx::mma_ts(o_tm, p_tm + kk * 8, vd + static_cast<uint64_t>(kk * (2048 >> 4)), IDESC_PV,
-                        1u);
+          for (int kk = 1; kk < C::BK / 32; ++kk)
+            ptx::mma_ts(o_tm, p_tm + kk * 8, vd + static_cast<uint64_t>(kk * (2048 >> 4)), IDESC_PV, 1u);
+          ptx::mma_commit(bar(C::B_PV + st));
+          if (!ptx::mbar_wait(bar(C::B_P + 2 * st + 1), phase, abort_flag, p.timeout_ns)) return false;
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int kk = C::BK / 32; kk < C::BK / 16; ++kk)
+            ptx::mma_ts(o_tm, p_tm + kk * 8, vd + static_cast<uint64_t>(kk * (2048 >> 4)), IDESC_PV, 1u);
           if (one || st == 1) ptx::mma_commit(bar(C::B_VE + slot));
           return true;
         };
@@ -799,8 +811,6 @@ __global__ void __launch_bounds__(384, 1)
       if (lane == 0) r = ptx::mbar_wait(b, parity, abort_flag, p.timeout_ns);
       return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
     };
-    // S of a block is issued behind the P V of the one before: O is quiet until
-    // P is handed on
     auto scale_o = [&](float alpha) {
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -884,7 +894,10 @@ __global__ void __launch_bounds__(384, 1)
           ptx::tmem_wait_st();
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar(C::B_P + st));
+          if (lane == 0) {
+            ptx::mbar_arrive(bar(C::B_P + 2 * st));
+            ptx::mbar_arrive(bar(C::B_P + 2 * st + 1));
+          }
         }
       } else {
         for (int i = 0; i < cnt; ++i) {
@@ -893,58 +906,72 @@ __global__ void __launch_bounds__(384, 1)
           ++steps;
           if (!ok) break;
           ptx::tc_fence_after();
-          if (active) {
-            uint32_t sv[128];
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            const bool cut = col0 + C::BK > least;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) ptx::tmem_ld32p(s_tm + 32 * c, sv + 32 * c);
+          if (!active) {
+            if (lane == 0) {
+              ptx::mbar_arrive(bar(C::B_P + 2 * st));
+              ptx::mbar_arrive(bar(C::B_P + 2 * st + 1));
+            }
+            continue;
+          }
+          // Two halves of 64 keys. Each takes its exponentials by the reference
+          // so far, with the maximum found beside them, and takes them again in
+          // the rare case that the reference has to move; its P is handed on at
+          // once, so that P V of the first half runs under the second's
+          // exponentials.
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t sv[64], pk[32];
+            ptx::tmem_ld32p(s_tm + 64 * h, sv);
+            ptx::tmem_ld32p(s_tm + 64 * h + 32, sv + 32);
             ptx::tmem_wait_ld();
-            if (cut) {
-              const int vis = limit - col0;
+            if (col0 + C::BK > least) {
+              const int vis = limit - col0 - 64 * h;
 #pragma unroll
-              for (int c = 0; c < 128; ++c)
+              for (int c = 0; c < 64; ++c)
                 if (c >= vis) sv[c] = __float_as_uint(-INFINITY);
             }
+            float sum;
+            for (;;) {
+              const float neg = mref == -INFINITY ? 0.0f : -mref;
+              float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < 128; c += 8) {
-              mx[0] = ptx::fmax3(mx[0], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-              mx[1] = ptx::fmax3(mx[1], __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
-              mx[2] = ptx::fmax3(mx[2], __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
-              mx[3] = ptx::fmax3(mx[3], __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
-            }
-            const float mb = fmaxf(ptx::fmax3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
-            const bool need = mb > mref + C::TAU;  // the first keys of a row always move it
-            if (__any_sync(0xffffffffu, need)) {
+              for (int j = 0; j < 64; j += 2) {
+                const float s0 = __uint_as_float(sv[j]), s1 = __uint_as_float(sv[j + 1]);
+                float x0, x1;
+                ptx::fma2(x0, x1, s0, s1, sl2, sl2, neg, neg);
+                const int m = (j >> 1) & 3, a = j & 6;
+                mx[m] = ptx::fmax3(mx[m], s0, s1);
+                const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+                ptx::add2(rs[a], rs[a + 1], rs[a], rs[a + 1], p0, p1);
+                pk[j / 2] = seq_pack2<T>(p0, p1);
+              }
+              sum = ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+              const float mb = fmaxf(ptx::fmax3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
+              const bool need = mb > mref + C::TAU;  // the first keys of a row always move it
+              if (!__any_sync(0xffffffffu, need)) break;
               const float mnew = need ? mb : mref;
               const float alpha = need ? ptx::ex2(mref - mnew) : 1.0f;  // 0 from -inf
               mref = mnew;
               l *= alpha;
-              if (i > 0) scale_o(alpha);
-            }
-            const float neg = mref == -INFINITY ? 0.0f : -mref;
-            float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t pk[16];
-#pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                float x0, x1;
-                ptx::fma2(x0, x1, __uint_as_float(sv[32 * c + j]), __uint_as_float(sv[32 * c + j + 1]),
-                          sl2, sl2, neg, neg);
-                const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
-                const int a = j & 6;
-                ptx::add2(rs[a], rs[a + 1], rs[a], rs[a + 1], p0, p1);
-                pk[j / 2] = seq_pack2<T>(p0, p1);
+              // O is quiet: S of this block was issued behind the P V of the one
+              // before, and the first half's is waited for
+              if (h == 1) {
+                ok = lane0_wait(bar(C::B_PV + st), (steps - 1) & 1);
+                if (!ok) break;
+                ptx::tc_fence_after();
               }
-              ptx::tmem_st16(s_tm + 16 * c, pk);
+              if (h == 1 || i > 0) scale_o(alpha);
             }
-            l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+            if (!ok) break;
+            ptx::tmem_st32(s_tm + 32 * h, pk);
+            l += sum;
             ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(C::B_P + 2 * st + h));
           }
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar(C::B_P + st));
+          if (!ok) break;
         }
       }
 
