@@ -152,6 +152,11 @@ __global__ void __launch_bounds__(256) blasst_seq_bwd_rows_kernel(const SeqBwdRo
   }
 }
 
+template <bool B>
+struct SeqBool {
+  static constexpr bool value = B;
+};
+
 template <int D>
 struct SeqBwdCfg {
   static constexpr int NTHREADS = 384;
@@ -572,174 +577,179 @@ __global__ void __launch_bounds__(384, 1)
     }
   } else {
     ptx::reg_take<C::REGS_SOFT>();
-    // ======================= P and dS ========================================
-    const int wg = warp >> 2;
-    const int row = (warp & 3) * 32 + lane;  // TMEM lane
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_tm = tmem + lane_base + C::S_COL + wg * 64;
-    const float sl2 = p.scale_log2;
-    bool ok = true;
-    // row item: the lane's token and statistics
-    const int tok = it.at + row / p.g;
-    const bool exists = key ? it.at + row < it.kvlen : row < box_rows && tok < it.qlen;
-    float nl2 = -INFINITY, dcol = 0.0f;
-    int limit = 0, least = 0;
-    if (!key) {
-      if (exists) {
-        const float2 v = p.stats[(static_cast<long long>(it.hk) * p.Tq + it.q0 + it.at) * p.g + row];
-        nl2 = v.x;
-        dcol = -v.y * c;
-      }
-      limit = p.causal ? min(it.off + tok + 1, it.kvlen) : it.kvlen;
-      least = p.causal ? min(it.off + it.at + 1, it.kvlen) : it.kvlen;
-    }
-    float pv[64];
-    // the lane's visible columns of tile i: [lo, hi), relative to the warpgroup's
-    auto columns = [&](int i, int& lo, int& hi) -> bool {
-      lo = 0;
-      hi = 64;
-      if (key) {
-        if (!p.causal) return false;
-        const int first = it.first + i * p.rt + it.off;  // key the tile's first token sees last
-        lo = max(it.at + row - first, 0) * p.g - wg * 64;
-        return it.at + C::BK - 1 > first;
-      }
-      const int col0 = i * C::BK;
-      hi = limit - col0 - wg * 64;
-      return col0 + C::BK > least;
-    };
-    auto form_p = [&](int i) -> bool {
-      if (!warp_wait(bar(C::B_S), i & 1)) return false;
-      if (key && !warp_wait(bar(C::B_STF + i % C::NST), (i / C::NST) & 1)) return false;
-      ptx::tc_fence_after();
-      uint32_t sv[64];
-      ptx::tmem_ld32p(s_tm, sv);
-      ptx::tmem_ld32p(s_tm + 32, sv + 32);
-      ptx::tmem_wait_ld();
+    // (compiled once per kind of item)
+    auto compute = [&](auto kind) {
+      constexpr bool key = decltype(kind)::value;
+      // ======================= P and dS ========================================
+      const int wg = warp >> 2;
+      const int row = (warp & 3) * 32 + lane;  // TMEM lane
+      const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t s_tm = tmem + lane_base + C::S_COL + wg * 64;
+      const float sl2 = p.scale_log2;
+      bool ok = true;
+      // row item: the lane's token and statistics
+      const int tok = it.at + row / p.g;
+      const bool exists = key ? it.at + row < it.kvlen : row < box_rows && tok < it.qlen;
+      float nl2 = -INFINITY, dcol = 0.0f;
+      int limit = 0, least = 0;
       if (!key) {
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(C::B_P));
+        if (exists) {
+          const float2 v = p.stats[(static_cast<long long>(it.hk) * p.Tq + it.q0 + it.at) * p.g + row];
+          nl2 = v.x;
+          dcol = -v.y * c;
+        }
+        limit = p.causal ? min(it.off + tok + 1, it.kvlen) : it.kvlen;
+        least = p.causal ? min(it.off + it.at + 1, it.kvlen) : it.kvlen;
       }
-      const float4* st = reinterpret_cast<const float4*>(smem + C::OFF_ST + (i % C::NST) * 1024) + wg * 16;
+      float pv[64];
+      // the lane's visible columns of tile i: [lo, hi), relative to the warpgroup's
+      auto columns = [&](int i, int& lo, int& hi) -> bool {
+        lo = 0;
+        hi = 64;
+        if (key) {
+          if (!p.causal) return false;
+          const int first = it.first + i * p.rt + it.off;  // key the tile's first token sees last
+          lo = max(it.at + row - first, 0) * p.g - wg * 64;
+          return it.at + C::BK - 1 > first;
+        }
+        const int col0 = i * C::BK;
+        hi = limit - col0 - wg * 64;
+        return col0 + C::BK > least;
+      };
+      auto form_p = [&](int i) -> bool {
+        if (!warp_wait(bar(C::B_S), i & 1)) return false;
+        if (key && !warp_wait(bar(C::B_STF + i % C::NST), (i / C::NST) & 1)) return false;
+        ptx::tc_fence_after();
+        uint32_t sv[64];
+        ptx::tmem_ld32p(s_tm, sv);
+        ptx::tmem_ld32p(s_tm + 32, sv + 32);
+        ptx::tmem_wait_ld();
+        if (!key) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(C::B_P));
+        }
+        const float4* st = reinterpret_cast<const float4*>(smem + C::OFF_ST + (i % C::NST) * 1024) + wg * 16;
 #pragma unroll
-      for (int j = 0; j < 64; j += 4) {
-        float4 a = make_float4(nl2, nl2, nl2, nl2);
-        if (key) a = st[j / 4];
-        float x0, x1, x2, x3;
-        ptx::fma2(x0, x1, __uint_as_float(sv[j]), __uint_as_float(sv[j + 1]), sl2, sl2, a.x, a.y);
-        ptx::fma2(x2, x3, __uint_as_float(sv[j + 2]), __uint_as_float(sv[j + 3]), sl2, sl2, a.z, a.w);
-        pv[j] = ptx::ex2(x0);
-        pv[j + 1] = ptx::ex2(x1);
-        pv[j + 2] = ptx::ex2(x2);
-        pv[j + 3] = ptx::ex2(x3);
-      }
-      int lo, hi;
-      if (columns(i, lo, hi)) {
+        for (int j = 0; j < 64; j += 4) {
+          float4 a = make_float4(nl2, nl2, nl2, nl2);
+          if (key) a = st[j / 4];
+          float x0, x1, x2, x3;
+          ptx::fma2(x0, x1, __uint_as_float(sv[j]), __uint_as_float(sv[j + 1]), sl2, sl2, a.x, a.y);
+          ptx::fma2(x2, x3, __uint_as_float(sv[j + 2]), __uint_as_float(sv[j + 3]), sl2, sl2, a.z, a.w);
+          pv[j] = ptx::ex2(x0);
+          pv[j + 1] = ptx::ex2(x1);
+          pv[j + 2] = ptx::ex2(x2);
+          pv[j + 3] = ptx::ex2(x3);
+        }
+        int lo, hi;
+        if (columns(i, lo, hi)) {
 #pragma unroll
-        for (int j = 0; j < 64; ++j)
-          if (j < lo || j >= hi) pv[j] = 0.0f;
-      }
-      if (key) {
+          for (int j = 0; j < 64; ++j)
+            if (j < lo || j >= hi) pv[j] = 0.0f;
+        }
+        if (key) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) pk[j] = seq_pack2<T>(pv[2 * j], pv[2 * j + 1]);
+          ptx::tmem_st32(s_tm, pk);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(C::B_P));
+        }
+        return true;
+      };
+      auto form_ds = [&](int i) -> bool {
+        if (!warp_wait(bar(C::B_DP + (i & 1)), (i >> 1) & 1)) return false;
+        ptx::tc_fence_after();
+        const uint32_t dp_tm =
+            tmem + lane_base + (key ? C::K_DP : C::R_DP + (i & 1) * 128) + wg * 64;
+        uint32_t dp[64];
+        ptx::tmem_ld32p(dp_tm, dp);
+        ptx::tmem_ld32p(dp_tm + 32, dp + 32);
+        ptx::tmem_wait_ld();
+        const float4* st =
+            reinterpret_cast<const float4*>(smem + C::OFF_ST + (i % C::NST) * 1024 + 512) + wg * 16;
+#pragma unroll
+        for (int j = 0; j < 64; j += 4) {
+          float4 a = make_float4(dcol, dcol, dcol, dcol);
+          if (key) a = st[j / 4];
+          float x[4];
+          ptx::fma2(x[0], x[1], __uint_as_float(dp[j]), __uint_as_float(dp[j + 1]), c, c, a.x, a.y);
+          ptx::fma2(x[2], x[3], __uint_as_float(dp[j + 2]), __uint_as_float(dp[j + 3]), c, c, a.z, a.w);
+          ptx::mul2(pv[j], pv[j + 1], x[0], x[1], pv[j], pv[j + 1]);
+          ptx::mul2(pv[j + 2], pv[j + 3], x[2], x[3], pv[j + 2], pv[j + 3]);
+        }
+        int lo, hi;
+        if (columns(i, lo, hi)) {  // a masked place may hold anything: 0, whatever dP is
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if (j < lo || j >= hi) pv[j] = 0.0f;
+        }
         uint32_t pk[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) pk[j] = seq_pack2<T>(pv[2 * j], pv[2 * j + 1]);
-        ptx::tmem_st32(s_tm, pk);
+        ptx::tmem_st32(dp_tm, pk);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(C::B_P));
-      }
-      return true;
-    };
-    auto form_ds = [&](int i) -> bool {
-      if (!warp_wait(bar(C::B_DP + (i & 1)), (i >> 1) & 1)) return false;
-      ptx::tc_fence_after();
-      const uint32_t dp_tm =
-          tmem + lane_base + (key ? C::K_DP : C::R_DP + (i & 1) * 128) + wg * 64;
-      uint32_t dp[64];
-      ptx::tmem_ld32p(dp_tm, dp);
-      ptx::tmem_ld32p(dp_tm + 32, dp + 32);
-      ptx::tmem_wait_ld();
-      const float4* st =
-          reinterpret_cast<const float4*>(smem + C::OFF_ST + (i % C::NST) * 1024 + 512) + wg * 16;
-      int lo, hi;
-      const bool cut = columns(i, lo, hi);
-      uint32_t pk[32];
-#pragma unroll
-      for (int j = 0; j < 64; j += 4) {
-        float4 a = make_float4(dcol, dcol, dcol, dcol);
-        if (key) a = st[j / 4];
-        float x[4];
-        ptx::fma2(x[0], x[1], __uint_as_float(dp[j]), __uint_as_float(dp[j + 1]), c, c, a.x, a.y);
-        ptx::fma2(x[2], x[3], __uint_as_float(dp[j + 2]), __uint_as_float(dp[j + 3]), c, c, a.z, a.w);
-        ptx::mul2(x[0], x[1], x[0], x[1], pv[j], pv[j + 1]);
-        ptx::mul2(x[2], x[3], x[2], x[3], pv[j + 2], pv[j + 3]);
-        if (cut) {  // a masked place may hold anything: 0, whatever dP is
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (j + u < lo || j + u >= hi) x[u] = 0.0f;
+        if (lane == 0) {
+          ptx::mbar_arrive(bar(C::B_DS + (i & 1)));
+          if (key) ptx::mbar_arrive(bar(C::B_STE + i % C::NST));
         }
-        pk[j / 2] = seq_pack2<T>(x[0], x[1]);
-        pk[j / 2 + 1] = seq_pack2<T>(x[2], x[3]);
+        return true;
+      };
+      if (n > 0) ok = form_p(0);
+      for (int i = 0; i < n && ok; ++i) {
+        ok = form_ds(i);
+        if (ok && i + 1 < n) ok = form_p(i + 1);
       }
-      ptx::tmem_st32(dp_tm, pk);
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        ptx::mbar_arrive(bar(C::B_DS + (i & 1)));
-        if (key) ptx::mbar_arrive(bar(C::B_STE + i % C::NST));
-      }
-      return true;
-    };
-    if (n > 0) ok = form_p(0);
-    for (int i = 0; i < n && ok; ++i) {
-      ok = form_ds(i);
-      if (ok && i + 1 < n) ok = form_p(i + 1);
-    }
-    if (ok && n > 0) ok = warp_wait(bar(C::B_ACC), 0);
-    ok = ok && *abort_flag == 0;
-    ok = __all_sync(0xffffffffu, ok) != 0;
-    if (!ok) {
-      fail();
-    } else {
-      ptx::tc_fence_after();
-      // key item: warpgroup 0 writes dV, 1 writes dK; row item: half of the
-      // columns of dQ each
-      const int chunks = key ? D / 32 : D / 64;
-      const int c0 = key ? 0 : wg * (D / 64);
-      const uint32_t acc = tmem + lane_base + (key ? (wg ? C::K_DK : C::K_DV) : C::R_DQ);
-      const float f = key && wg == 0 ? p.p_unscale : p.scale * ds_unscale;
-      T* out;
-      if (key) out = static_cast<T*>(wg ? p.dk : p.dv) +
-                     (static_cast<long long>(it.k0 + it.at + row) * p.Hkv + it.hk) * D;
-      else out = static_cast<T*>(p.dq) +
-                 (static_cast<long long>(it.q0 + tok) * p.Hq + it.hk * p.g + row % p.g) * D;
+      if (ok && n > 0) ok = warp_wait(bar(C::B_ACC), 0);
+      ok = ok && *abort_flag == 0;
+      ok = __all_sync(0xffffffffu, ok) != 0;
+      if (!ok) {
+        fail();
+      } else {
+        ptx::tc_fence_after();
+        // key item: warpgroup 0 writes dV, 1 writes dK; row item: half of the
+        // columns of dQ each
+        const int chunks = key ? D / 32 : D / 64;
+        const int c0 = key ? 0 : wg * (D / 64);
+        const uint32_t acc = tmem + lane_base + (key ? (wg ? C::K_DK : C::K_DV) : C::R_DQ);
+        const float f = key && wg == 0 ? p.p_unscale : p.scale * ds_unscale;
+        T* out;
+        if (key) out = static_cast<T*>(wg ? p.dk : p.dv) +
+                       (static_cast<long long>(it.k0 + it.at + row) * p.Hkv + it.hk) * D;
+        else out = static_cast<T*>(p.dq) +
+                   (static_cast<long long>(it.q0 + tok) * p.Hq + it.hk * p.g + row % p.g) * D;
 #pragma unroll 1
-      for (int k = c0; k < c0 + chunks; ++k) {
-        uint32_t r[32];
-        if (n > 0) {
-          ptx::tmem_ld32(acc + 32 * k, r);
-          ptx::tmem_wait_ld();
-        } else {
+        for (int k = c0; k < c0 + chunks; ++k) {
+          uint32_t r[32];
+          if (n > 0) {
+            ptx::tmem_ld32(acc + 32 * k, r);
+            ptx::tmem_wait_ld();
+          } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = 0u;
-        }
-        if (exists) {
-          uint4* dst = reinterpret_cast<uint4*>(out + 32 * k);
+            for (int j = 0; j < 32; ++j) r[j] = 0u;
+          }
+          if (exists) {
+            uint4* dst = reinterpret_cast<uint4*>(out + 32 * k);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              w[u] = seq_pack2<T>(__uint_as_float(r[8 * j + 2 * u]) * f,
-                                  __uint_as_float(r[8 * j + 2 * u + 1]) * f);
-            dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int u = 0; u < 4; ++u)
+                w[u] = seq_pack2<T>(__uint_as_float(r[8 * j + 2 * u]) * f,
+                                    __uint_as_float(r[8 * j + 2 * u + 1]) * f);
+              dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
         }
       }
-    }
+    };
+    if (key) compute(SeqBool<true>{});
+    else compute(SeqBool<false>{});
   }
 
   __syncwarp();
