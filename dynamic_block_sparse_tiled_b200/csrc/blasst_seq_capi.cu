@@ -211,13 +211,15 @@ bool rotary_vec(int d, int rot, bool interleaved, int vec) {
 
 template <typename T, int VEC>
 int launch_rotary(const blasst::RotaryParams& p, dim3 grid, size_t smem, cudaStream_t s) {
-  blasst::blasst_rotary_kernel<T, VEC><<<grid, 256, smem, s>>>(p);
+  if (p.interleaved) blasst::blasst_rotary_kernel<T, VEC, true><<<grid, 256, smem, s>>>(p);
+  else blasst::blasst_rotary_kernel<T, VEC, false><<<grid, 256, smem, s>>>(p);
   return cuda_status(cudaGetLastError());
 }
 
 template <typename T, int VEC>
 int launch_append(const blasst::AppendParams& p, dim3 grid, size_t smem, cudaStream_t s) {
-  blasst::blasst_append_kernel<T, VEC><<<grid, 256, smem, s>>>(p);
+  if (p.interleaved) blasst::blasst_append_kernel<T, VEC, true><<<grid, 256, smem, s>>>(p);
+  else blasst::blasst_append_kernel<T, VEC, false><<<grid, 256, smem, s>>>(p);
   return cuda_status(cudaGetLastError());
 }
 
@@ -279,11 +281,16 @@ int blasst_rotary(const blasst_rotary_args* a) {
   const bool wide = rotary_vec(a->d, a->rot, p.interleaved, vec) &&
                     vector_ok(a->x, sx, 3, vec, eb) && vector_ok(a->y, sy, 3, vec, eb);
   const int places = blasst::rotary_places(a->d, a->rot, p.interleaved, wide ? vec : 1);
-  // four tokens per block share the set-up when there are enough of them
-  p.tb = tokens >= 16ll * sms ? 4 : 1;
+  // as many tokens per block as leave a thread one round of loads, while there
+  // are blocks enough; few tokens: heads over blocks
+  const int groups = std::max(1, 256 / std::min(places, 256));
+  p.tb = 1;
+  while (2 * p.tb <= groups && groups / (2 * p.tb) * blasst::kRotaryAhead >= a->H &&
+         tokens >= 16ll * p.tb * sms)
+    p.tb *= 2;
   const long long blocks = (tokens + p.tb - 1) / p.tb;
   if (blocks > 0x7fffffffll) return BLASST_EINVAL;
-  p.hb = heads_per_block(blocks, a->H, places, sms);
+  p.hb = p.tb > 1 ? a->H : heads_per_block(blocks, a->H, places, sms);
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((a->H + p.hb - 1) / p.hb));
   if (grid.y > 65535) return BLASST_EINVAL;
   const size_t smem = static_cast<size_t>(p.tb) * (a->rot / 2) * sizeof(float2);
