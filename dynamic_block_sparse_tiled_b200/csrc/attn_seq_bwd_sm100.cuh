@@ -86,6 +86,7 @@ constexpr int kBwdRowsPerBlock = 64;
 // takes two rows at a time, 16 lanes each (8 values = 16 bytes per lane and step).
 template <int D, typename T>
 __global__ void __launch_bounds__(256) blasst_seq_bwd_rows_kernel(const SeqBwdRowsParams p) {
+  ptx::grid_launch_dependents();     // (the pair kernel waits before it reads what is written here)
   constexpr int LPR = D / 8;         // lanes per row
   constexpr int RPW = 32 / LPR;      // rows per warp
   const int hk = blockIdx.y;
@@ -231,6 +232,7 @@ __global__ void __launch_bounds__(384, 1)
   const int lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
   if ((sb & 1023u) != 0u) {  // uniform; the tiles need 1 KB alignment
+    ptx::grid_wait();
     if (threadIdx.x == 0) seq_record_error(p.err, BLASST_EUNSUPPORTED);
     return;
   }
@@ -333,7 +335,10 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   SeqBwdItem it;
   it.kind = itemw[0];
-  if (it.kind == 0) return;  // uniform, nothing in flight
+  if (it.kind == 0) {  // uniform, nothing in flight
+    ptx::grid_wait();    // (the row pass ends before this kernel does)
+    return;
+  }
   it.hk = itemw[1];
   it.q0 = itemw[2];
   it.qlen = itemw[3];
@@ -372,6 +377,7 @@ __global__ void __launch_bounds__(384, 1)
     if (lane == 0) r = ptx::mbar_wait(b, parity, abort_flag, p.timeout_ns);
     return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
   };
+  ptx::grid_wait();  // the rows' statistics (the set-up ran beside their pass)
   // dS = (2^shift P) (c dP - c D) = 2^k P (dP - D)
   float c = 1.0f, ds_unscale = 1.0f;
   if (p.norms && n > 0) {

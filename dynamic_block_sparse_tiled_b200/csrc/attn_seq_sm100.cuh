@@ -183,6 +183,7 @@ struct SeqAttnCfg {
 // constant for its start and end
 constexpr int kSeqItemCost = 4;
 constexpr int kSeqMinRange = 10;  // every range inside an item then holds a block's start
+constexpr int kSeqMostPiece = 8;  // little work: most blocks of an item per CTA
 
 __device__ __forceinline__ int seq_blocks(const SeqSpan& q, int causal, int tok) {
   const int keys = causal ? min(max(q.off + tok + 1, 0), q.kvlen) : q.kvlen;
@@ -205,13 +206,23 @@ __device__ __forceinline__ SeqItem seq_item(const SeqSpan& q, int causal, int rt
   return it;
 }
 
-__device__ __forceinline__ long long seq_cost(const SeqSpan& q, int causal, int rt, int it_tok) {
-  long long c = 0;
+// Of one KV head of a sequence: its cost, items and key blocks.
+struct SeqCost {
+  long long cost, items, blocks;
+};
+__device__ __forceinline__ SeqCost seq_cost(const SeqSpan& q, int causal, int rt, int it_tok) {
+  SeqCost c{0, q.tiles, 0};
   for (int t = 0; t < q.tiles; ++t) {
     const SeqItem it = seq_item(q, causal, rt, it_tok, t);
-    c += kSeqItemCost + static_cast<long long>(it.nblk) * it.unit;
+    c.cost += kSeqItemCost + static_cast<long long>(it.nblk) * it.unit;
+    c.blocks += it.nblk;
   }
   return c;
+}
+
+// Pieces of up to r blocks of an item (an item without blocks is one).
+__device__ __forceinline__ int seq_pieces(const SeqItem& it, int r) {
+  return it.nblk <= r ? 1 : static_cast<int>(static_cast<uint32_t>(it.nblk + r - 1) / static_cast<uint32_t>(r));
 }
 
 // a / b of non-negative numbers; 64-bit division only where it is needed (it
@@ -467,14 +478,64 @@ __global__ void __launch_bounds__(384, 1)
         load_chunk(s & ~31);
         return seq_span_of(mine, s & 31);
       };
-      long long total = 0, own = 0;
-      for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
-        load_chunk(s0);
-        own = seq_cost(mine, p.causal, p.rt, p.it_tok) * p.Hkv;
-        long long c = own;
+      long long total = 0, items = 0, blocks = 0, own = 0;
+      auto add_up = [&](long long c) -> long long {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
-        total += c;
+        return c;
+      };
+      for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
+        load_chunk(s0);
+        const SeqCost c = seq_cost(mine, p.causal, p.rt, p.it_tok);
+        own = c.cost * p.Hkv;
+        total += add_up(own);
+        items += add_up(c.items) * p.Hkv;
+        blocks += add_up(c.blocks) * p.Hkv;
+      }
+      // Little work (an eighth of a CTA's worth of items to spare, few blocks
+      // each): every CTA one piece of one item, so that none has to start
+      // another item behind its first.
+      const long long spare = static_cast<long long>(gridDim.x) - items;
+      const long long piece = spare > 0 ? max(2ll, seq_div(blocks + spare - 1, spare)) : 0;
+      const bool little = 8 * spare >= gridDim.x && piece <= kSeqMostPiece;
+      if (little) {
+        const int r = static_cast<int>(piece);
+        long long at = 0;
+        for (int s0 = 0; s0 < p.n_seq && live; s0 += 32) {
+          load_chunk(s0);
+          long long np = 0;
+          for (int t = 0; t < mine.tiles; ++t)
+            np += seq_pieces(seq_item(mine, p.causal, p.rt, p.it_tok, t), r);
+          long long upto = np * p.Hkv;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += v;
+          }
+          const uint32_t hit = __ballot_sync(0xffffffffu, blockIdx.x < at + upto);
+          if (hit) {
+            const int l = __ffs(hit) - 1;
+            np = __shfl_sync(0xffffffffu, np, l);
+            int left = static_cast<int>(blockIdx.x - (at + __shfl_sync(0xffffffffu, upto, l) - np * p.Hkv));
+            const int h = left / static_cast<int>(np);
+            left -= h * static_cast<int>(np);
+            const SeqSpan q = seq_span_of(mine, l);
+            SeqItem it = seq_item(q, p.causal, p.rt, p.it_tok, 0);
+            int n_pieces = seq_pieces(it, r);
+            for (int t = 1; left >= n_pieces; ++t) {
+              left -= n_pieces;
+              it = seq_item(q, p.causal, p.rt, p.it_tok, t);
+              n_pieces = seq_pieces(it, r);
+            }
+            if (lane == 0 && left == 0 && n_pieces > 1) {
+              p.part_desc[2 * blockIdx.x] = make_int4(q.q0 + it.tok0, it.ntok, h, it.one ? 1 : 0);
+              p.part_desc[2 * blockIdx.x + 1] = make_int4(blockIdx.x + n_pieces - 1, 0, 0, 0);
+            }
+            ok = put(s0 + l, q, h, it, left * r, min(left * r + r, it.nblk));
+            break;
+          }
+          at += __shfl_sync(0xffffffffu, upto, 31);
+        }
       }
       const long long share = seq_div(total + gridDim.x - 1, gridDim.x);
       const long long range = share < kSeqMinRange ? kSeqMinRange : share;
@@ -483,10 +544,10 @@ __global__ void __launch_bounds__(384, 1)
       long long at = 0;  // the list's place of what is looked at
       int s = 0, h = 0, t = 0;
       bool found = false;
-      for (int s0 = 0; s0 < p.n_seq && !found && live && lo < total; s0 += 32) {
+      for (int s0 = 0; s0 < p.n_seq && !found && !little && live && lo < total; s0 += 32) {
         if (s0 != chunk) {
           load_chunk(s0);
-          own = seq_cost(mine, p.causal, p.rt, p.it_tok) * p.Hkv;
+          own = seq_cost(mine, p.causal, p.rt, p.it_tok).cost * p.Hkv;
         }
         long long upto = own;
 #pragma unroll
@@ -1131,23 +1192,30 @@ __global__ void __launch_bounds__(256) blasst_seq_join_kernel(const SeqAttnParam
   for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
     const int tok = (r >> 7) * p.rt + (r & 127) / p.g;
     if ((r & 127) >= p.g * p.rt || tok >= d.y) continue;
-    float m = -INFINITY, l = 0.0f, acc[V];
+    auto row_of = [&](int k) -> size_t { return static_cast<size_t>(2 * k + (k == c ? 1 : 0)) * 256 + r; };
+    float m = -INFINITY, x = -INFINITY;
+    for (int k0 = c; k0 <= last; k0 += 32) {  // one part per lane
+      x = k0 + lane <= last ? p.part_lse[row_of(k0 + lane)] : -INFINITY;
+      float most = x;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, s));
+      m = fmaxf(m, most);
+    }
+    float l = 0.0f, acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-    for (int k = c; k <= last; ++k) {
-      const size_t row = static_cast<size_t>(2 * k + (k == c ? 1 : 0)) * 256 + r;
-      const float x = p.part_lse[row];
-      const float* src = p.part_o + row * D + lane * V;
-      float o[V];
+    for (int k0 = c; k0 <= last; k0 += 32) {
+      if (last - c >= 32) x = k0 + lane <= last ? p.part_lse[row_of(k0 + lane)] : -INFINITY;
+      const float own = x == -INFINITY ? 0.0f : ptx::ex2(x - m);
+      const int n = min(32, last - k0 + 1);
+#pragma unroll 4
+      for (int k = 0; k < n; ++k) {
+        const float w = __shfl_sync(0xffffffffu, own, k);
+        const float* src = p.part_o + row_of(k0 + k) * D + lane * V;
+        l += w;
 #pragma unroll
-      for (int v = 0; v < V; ++v) o[v] = src[v];
-      if (x == -INFINITY) continue;
-      const float mn = fmaxf(m, x);
-      const float a = m == -INFINITY ? 0.0f : ptx::ex2(m - mn), w = ptx::ex2(x - mn);
-      m = mn;
-      l = l * a + w;
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = acc[v] * a + w * o[v];
+        for (int v = 0; v < V; ++v) acc[v] = w == 0.0f ? acc[v] : fmaf(w, src[v], acc[v]);
+      }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const long long out = static_cast<long long>(d.x + tok) * p.Hq + d.z * p.g + (r & 127) % p.g;

@@ -77,6 +77,23 @@ int check_regs(K kernel, int regs, int& known) {
   return known >= regs ? BLASST_OK : BLASST_EUNSUPPORTED;
 }
 
+// A launch that may begin while the kernel before it runs; the kernel waits for
+// that one's end itself.
+template <typename K, typename... A>
+cudaError_t launch_early(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = grid;
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, args...);
+}
+
 template <int D, typename T, bool FEW>
 int launch_seq(const CUtensorMap& mq, const CUtensorMap& mq_few, const CUtensorMap& mk,
                const CUtensorMap& mv, const blasst::SeqAttnParams& p, int sms, cudaStream_t stream) {
@@ -93,17 +110,7 @@ int launch_seq(const CUtensorMap& mq, const CUtensorMap& mq_few, const CUtensorM
   kernel<<<grid, C::NTHREADS, C::SMEM_BYTES, stream>>>(mq, mq_few, mk, mv, p);
   int rc = cuda_status(cudaGetLastError());
   if (rc != BLASST_OK || !shared_list) return rc;
-  // launched while the first kernel runs, waits for its end itself
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t join{};
-  join.gridDim = dim3(grid, 4);
-  join.blockDim = dim3(256);
-  join.stream = stream;
-  join.attrs = &early;
-  join.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&join, blasst::blasst_seq_join_kernel<D, T>, p));
+  return cuda_status(launch_early(blasst::blasst_seq_join_kernel<D, T>, dim3(grid, 4), 256, 0, stream, p));
 }
 
 template <int D, typename T>
@@ -190,6 +197,8 @@ int launch_seq_bwd(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensor
     if (rc != BLASST_OK) return rc;
   }
   const unsigned grid = static_cast<unsigned>(p.n_key + p.n_row) * p.Hkv;
+  if (r.Tq > 0)
+    return cuda_status(launch_early(kernel, dim3(grid), C::NTHREADS, C::SMEM_BYTES, stream, mq, mdo, mk, mv, p));
   kernel<<<grid, C::NTHREADS, C::SMEM_BYTES, stream>>>(mq, mdo, mk, mv, p);
   return cuda_status(cudaGetLastError());
 }
