@@ -311,6 +311,11 @@ __device__ __forceinline__ void seq_few_take(const float* x, T* o, float* part) 
   }
 }
 
+template <int ST>
+struct SeqStream {
+  static constexpr int value = ST;
+};
+
 template <int D, typename T, bool FEW>
 __global__ void __launch_bounds__(384, 1)
     blasst_seq_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -767,85 +772,103 @@ __global__ void __launch_bounds__(384, 1)
     }
   } else if (warp == C::WARP_MMA) {
     // ======================= tcgen05 issuer ================================
+    // What this thread does between two products is time the tensor core does
+    // not work: ring places are kept as counters, descriptors are ready before
+    // the waits, and a block that both streams use is waited for once.
     if (lane == 0) {
       bool ok = true;
       const uint64_t q_desc = ptx::sw128_desc(sb + C::OFF_Q, 16, 1024);
       const uint64_t k_desc = ptx::sw128_desc(sb + C::OFF_K, 16, 1024);
       const uint64_t v_desc = ptx::sw128_desc(sb + C::OFF_V, C::BOX, 1024);
-      uint32_t ring0 = 0;                 // ring position of the item's first blocks
-      uint32_t steps[2] = {0, 0};         // blocks done per stream (P phases)
+      constexpr uint64_t TS = C::TILE >> 4;
+      uint32_t k_slot = 0, k_turn = 0, v_slot = 0, v_turn = 0;  // newest blocks, phase parity
+      uint64_t kd = k_desc, vd = v_desc;                        // of those slots
+      uint32_t phase[2] = {0, 0};                               // of P, per stream
       SeqRecord it;
+      auto wait = [&](int b, uint32_t parity) -> bool {
+        return ptx::mbar_wait(bar(b), parity, abort_flag, p.timeout_ns);
+      };
       for (int n = 0; ok; ++n) {
         ok = next_item(n, it);
         if (!ok) break;
         item_read(n);
         if (it.seq < 0) break;
-        const int nb = it.nb;
         const bool one = it.one();
-        const int cnt[2] = {it.cnt(0), it.cnt(1)};
-        ok = ptx::mbar_wait(bar(C::B_Q), n & 1, abort_flag, p.timeout_ns);
+        const int cnt0 = it.cnt(0), cnt1 = it.cnt(1);
+        ok = wait(C::B_Q, n & 1);
         if (!ok) break;
-        auto issue_s = [&](int st, int i) -> bool {
-          const int b = one ? 2 * i + st : i;
-          const uint32_t k = ring0 + b;
-          const uint32_t slot = k % C::NK;
-          // (a block both streams use is waited for once: every look at a barrier
-          // costs this thread as much as a product)
-          if ((one || st == 0 || i >= cnt[0]) &&
-              !ptx::mbar_wait(bar(C::B_KF + slot), (k / C::NK) & 1, abort_flag, p.timeout_ns))
-            return false;
+        // S of stream st; `first`: of the streams that use the block, `last` too
+        auto issue_s = [&](auto stream, bool first, bool last) -> bool {
+          constexpr int st = decltype(stream)::value;
+          const uint64_t qd = q_desc + (st == 1 && !one ? TS : 0);
+          if (first && !wait(C::B_KF + k_slot, k_turn)) return false;
           ptx::tc_fence_after();
-          const uint64_t qd =
-              q_desc + static_cast<uint64_t>(one ? 0 : st * (C::TILE >> 4));
-          const uint64_t kd = k_desc + static_cast<uint64_t>(slot * (C::TILE >> 4));
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t o = static_cast<uint64_t>(((kk >> 2) * C::BOX + (kk & 3) * 32) >> 4);
             ptx::mma_ss(tmem + C::S_COL + st * 128, qd + o, kd + o, IDESC_S, kk > 0 ? 1u : 0u);
           }
           ptx::mma_commit(bar(C::B_S + st));
-          if (one || st == 1) ptx::mma_commit(bar(C::B_KE + slot));
+          if (last) {
+            ptx::mma_commit(bar(C::B_KE + k_slot));
+            kd += TS;
+            if (++k_slot == C::NK) {
+              k_slot = 0;
+              k_turn ^= 1u;
+              kd = k_desc;
+            }
+          }
           return true;
         };
-        auto issue_pv = [&](int st, int i) -> bool {
-          const int b = one ? 2 * i + st : i;
-          const uint32_t k = ring0 + b;
-          const uint32_t slot = k % C::NV;
-          // the first half of the keys as soon as its P is there
-          const uint32_t phase = steps[st]++ & 1;
-          if ((one || st == 0 || i >= cnt[0]) &&
-              !ptx::mbar_wait(bar(C::B_VF + slot), (k / C::NV) & 1, abort_flag, p.timeout_ns))
-            return false;
-          if (!ptx::mbar_wait(bar(C::B_P + 2 * st), phase, abort_flag, p.timeout_ns)) return false;
-          ptx::tc_fence_after();
-          const uint64_t vd = v_desc + static_cast<uint64_t>(slot * (C::TILE >> 4));
+        auto issue_pv = [&](auto stream, int i, bool first, bool last) -> bool {
+          constexpr int st = decltype(stream)::value;
           const uint32_t o_tm = tmem + C::O_COL + st * D;
           const uint32_t p_tm = tmem + C::S_COL + st * 128;
+          if (first && !wait(C::B_VF + v_slot, v_turn)) return false;
+          // the first half of the keys as soon as its P is there
+          if (!wait(C::B_P + 2 * st, phase[st])) return false;
+          ptx::tc_fence_after();
           ptx::mma_ts(o_tm, p_tm, vd, IDESC_PV, i > 0 ? 1u : 0u);
 #pragma unroll
           for (int kk = 1; kk < C::BK / 32; ++kk)
             ptx::mma_ts(o_tm, p_tm + kk * 8, vd + static_cast<uint64_t>(kk * (2048 >> 4)), IDESC_PV, 1u);
           ptx::mma_commit(bar(C::B_PV + st));
-          if (!ptx::mbar_wait(bar(C::B_P + 2 * st + 1), phase, abort_flag, p.timeout_ns)) return false;
+          if (!wait(C::B_P + 2 * st + 1, phase[st])) return false;
           ptx::tc_fence_after();
 #pragma unroll
           for (int kk = C::BK / 32; kk < C::BK / 16; ++kk)
             ptx::mma_ts(o_tm, p_tm + kk * 8, vd + static_cast<uint64_t>(kk * (2048 >> 4)), IDESC_PV, 1u);
-          if (one || st == 1) ptx::mma_commit(bar(C::B_VE + slot));
+          phase[st] ^= 1u;
+          if (last) {
+            ptx::mma_commit(bar(C::B_VE + v_slot));
+            vd += TS;
+            if (++v_slot == C::NV) {
+              v_slot = 0;
+              v_turn ^= 1u;
+              vd = v_desc;
+            }
+          }
           return true;
         };
-        for (int st = 0; st < 2 && ok; ++st)
-          if (cnt[st] > 0) ok = issue_s(st, 0);
+        // two tiles: stream 1 sees every block, stream 0 the first cnt0 of them
+        const SeqStream<0> s0;
+        const SeqStream<1> s1;
+        if (cnt0 > 0) ok = issue_s(s0, true, one);
+        if (ok && cnt1 > 0) ok = issue_s(s1, one || cnt0 == 0, true);
         // O is free once the item before has been read out
-        if (ok && n > 0) ok = ptx::mbar_wait(bar(C::B_OFREE), (n - 1) & 1, abort_flag, p.timeout_ns);
-        const int most = max(cnt[0], cnt[1]);
-        for (int i = 0; i < most && ok; ++i)
-          for (int st = 0; st < 2 && ok; ++st) {
-            if (i < cnt[st]) ok = issue_pv(st, i);
-            if (ok && i + 1 < cnt[st]) ok = issue_s(st, i + 1);
+        if (ok && n > 0) ok = wait(C::B_OFREE, (n - 1) & 1);
+        const int most = max(cnt0, cnt1);
+        for (int i = 0; i < most && ok; ++i) {
+          if (i < cnt0) {
+            ok = issue_pv(s0, i, true, one);
+            if (ok && i + 1 < cnt0) ok = issue_s(s0, true, one);
           }
+          if (ok && i < cnt1) {
+            ok = issue_pv(s1, i, one || i >= cnt0, true);
+            if (ok && i + 1 < cnt1) ok = issue_s(s1, one || i + 1 >= cnt0, true);
+          }
+        }
         ptx::mma_commit(bar(C::B_DONE));
-        ring0 += nb;
       }
       if (!ok) fail();
       // every product has completed before TMEM is freed
