@@ -82,62 +82,72 @@ struct SeqBwdRowsParams {
 constexpr int kBwdRowsPerBlock = 64;
 
 // Row pass: D_i and the scaled lse of every row, laid out so that a tile's
-// rows are contiguous; with `norms` the largest rows of dO and v too. A warp
-// takes two rows at a time, 16 lanes each (8 values = 16 bytes per lane and step).
+// rows are contiguous; with `norms` the largest rows of dO and v too. D / 8
+// lanes per row (16 bytes each), every warp all its rows' loads at once.
+// Bound by memory: o and dO read once.
 template <int D, typename T>
 __global__ void __launch_bounds__(256) blasst_seq_bwd_rows_kernel(const SeqBwdRowsParams p) {
   ptx::grid_launch_dependents();     // (the pair kernel waits before it reads what is written here)
   constexpr int LPR = D / 8;         // lanes per row
   constexpr int RPW = 32 / LPR;      // rows per warp
+  constexpr int N = kBwdRowsPerBlock / (8 * RPW);
   const int hk = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPR, at = lane % LPR;
-  float most = 0.0f;
   const bool of_v = static_cast<int>(blockIdx.x) >= p.row_blocks;
   const long long block = of_v ? blockIdx.x - p.row_blocks : blockIdx.x;
   const long long all = static_cast<long long>(p.Tq) * p.g;
   // what belongs to no sequence is not read (it may hold anything)
   const int* cu = of_v ? p.cu_k : p.cu_q;
-  const int per = of_v ? 1 : p.g;
+  const uint32_t per = of_v ? 1 : p.g;
   const long long begin = static_cast<long long>(max(cu[0], 0)) * per;
   const long long end = static_cast<long long>(min(cu[p.n_seq], of_v ? p.Tk : p.Tq)) * per;
+  uint4 av[N], bv[N];
+  float lse[N];
 #pragma unroll
-  for (int i = 0; i < kBwdRowsPerBlock / (8 * RPW); ++i) {
+  for (int i = 0; i < N; ++i) {
     const long long r = block * kBwdRowsPerBlock + (i * 8 + warp) * RPW + sub;
-    float dot = 0.0f, sq = 0.0f;
-    const bool owned = r >= begin && r < end;
-    if (owned) {
-      const T* a;
-      const T* b;
-      if (of_v) {
-        a = b = static_cast<const T*>(p.v) + r * p.v_st + hk * p.v_sh + at * 8;
-      } else {
-        const long long t = r / p.g, h = hk * p.g + r % p.g;
-        a = static_cast<const T*>(p.dout) + t * p.do_st + h * p.do_sh + at * 8;
-        b = static_cast<const T*>(p.o) + t * p.o_st + h * p.o_sh + at * 8;
-      }
-      uint4 av = *reinterpret_cast<const uint4*>(a), bv = *reinterpret_cast<const uint4*>(b);
-      const T* ae = reinterpret_cast<const T*>(&av);
-      const T* be = reinterpret_cast<const T*>(&bv);
+    av[i] = bv[i] = make_uint4(0u, 0u, 0u, 0u);
+    lse[i] = 0.0f;
+    if (r < begin || r >= end) continue;
+    if (of_v) {
+      av[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + r * p.v_st + hk * p.v_sh + at * 8);
+    } else {
+      // (rows count below 2^38; within a KV head 32 bits hold tokens and heads)
+      const long long t = all >> 32 ? r / per : static_cast<uint32_t>(r) / per;
+      const int h = hk * p.g + static_cast<int>(r - t * per);
+      av[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.dout) + t * p.do_st + h * p.do_sh + at * 8);
+      bv[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.o) + t * p.o_st + h * p.o_sh + at * 8);
+      if (at == 0) lse[i] = p.lse[t * p.Hq + h];
+    }
+  }
+  float most = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = static_cast<float>(ae[j]);
-        dot = fmaf(x, static_cast<float>(be[j]), dot);
-        sq = fmaf(x, x, sq);
-      }
-    }
+  for (int i = 0; i < N; ++i) {
+    const long long r = block * kBwdRowsPerBlock + (i * 8 + warp) * RPW + sub;
+    const uint32_t aw[4] = {av[i].x, av[i].y, av[i].z, av[i].w};
+    const uint32_t bw[4] = {bv[i].x, bv[i].y, bv[i].z, bv[i].w};
+    float dot0 = 0.0f, dot1 = 0.0f, sq0 = 0.0f, sq1 = 0.0f;
 #pragma unroll
-    for (int d = LPR / 2; d > 0; d >>= 1) {
-      dot += __shfl_xor_sync(0xffffffffu, dot, d);
-      sq += __shfl_xor_sync(0xffffffffu, sq, d);
+    for (int j = 0; j < 4; ++j) {
+      float a0, a1, b0, b1;
+      seq_unpack2<T>(aw[j], a0, a1);
+      seq_unpack2<T>(bw[j], b0, b1);
+      ptx::fma2(dot0, dot1, a0, a1, b0, b1, dot0, dot1);
+      if (p.norms) ptx::fma2(sq0, sq1, a0, a1, a0, a1, sq0, sq1);
     }
-    if (owned && !of_v && at == 0) {
-      const long long t = r / p.g, h = hk * p.g + r % p.g;
-      const float l = p.lse[t * p.Hq + h];
-      p.stats[static_cast<long long>(hk) * all + r] =
-          make_float2(l == -INFINITY ? -INFINITY : fmaf(l, -1.4426950408889634f, p.shift), dot);
+    float dot = dot0 + dot1;
+#pragma unroll
+    for (int d = LPR / 2; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+    if (p.norms) {
+      float sq = sq0 + sq1;
+#pragma unroll
+      for (int d = LPR / 2; d > 0; d >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, d);
+      most = fmaxf(most, sq);
     }
-    most = fmaxf(most, sq);
+    if (at == 0 && !of_v && r >= begin && r < end)
+      p.stats[static_cast<long long>(hk) * all + r] = make_float2(
+          lse[i] == -INFINITY ? -INFINITY : fmaf(lse[i], -1.4426950408889634f, p.shift), dot);
   }
   if (p.norms) {
 #pragma unroll

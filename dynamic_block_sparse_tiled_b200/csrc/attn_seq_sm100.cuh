@@ -265,6 +265,19 @@ __device__ __forceinline__ uint32_t seq_pack2<__half>(float lo, float hi) {
   return ptx::pack_f16x2(lo, hi);
 }
 template <typename T>
+__device__ __forceinline__ void seq_unpack2(uint32_t w, float& lo, float& hi);
+template <>
+__device__ __forceinline__ void seq_unpack2<__nv_bfloat16>(uint32_t w, float& lo, float& hi) {
+  lo = __uint_as_float(w << 16);
+  hi = __uint_as_float(w & 0xffff0000u);
+}
+template <>
+__device__ __forceinline__ void seq_unpack2<__half>(uint32_t w, float& lo, float& hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  lo = f.x;
+  hi = f.y;
+}
+template <typename T>
 struct SeqType;
 template <>
 struct SeqType<__nv_bfloat16> {

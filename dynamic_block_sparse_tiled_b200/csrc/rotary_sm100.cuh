@@ -276,7 +276,8 @@ __global__ void __launch_bounds__(256) blasst_append_kernel(const AppendParams p
           const long long cap = static_cast<long long>(p.table_width) * p.page_size;
           placed = q0 >= 0 && q1 <= p.T && pos >= 0 && pos < cap;
           if (placed) {
-            const int in_table = static_cast<int>(pos / p.page_size);
+            // (a position is below 2^31: it counts from a 32-bit length)
+            const uint32_t in_table = static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page_size);
             page = p.table[static_cast<long long>(s) * p.table_stride + in_table];
             row = pos - static_cast<long long>(in_table) * p.page_size;
             placed = page >= 0 && page < p.n_pages;
