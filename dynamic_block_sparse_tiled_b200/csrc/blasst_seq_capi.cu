@@ -386,10 +386,14 @@ int blasst_append(const blasst_append_args* a) {
   if (a->q) wide = wide && vector_ok(a->q, sq, 4, vec, eb) && vector_ok(a->q_out, sq, 4, vec, eb);
   const int places = blasst::rotary_places(a->d, a->rot, p.interleaved, wide ? vec : 1);
   const int heads = (a->q ? a->Hq : 0) + 2 * a->Hkv;
-  p.hb = heads_per_block(a->T, heads, places, sms);
-  const dim3 grid(static_cast<unsigned>(a->T), static_cast<unsigned>((heads + p.hb - 1) / p.hb));
+  const int groups = std::max(1, 256 / std::min(places, 256));
+  p.tb = 1;
+  while (2 * p.tb <= std::min(groups, blasst::kAppendTokens) && a->T >= 8ll * p.tb * sms) p.tb *= 2;
+  const int blocks = (a->T + p.tb - 1) / p.tb;
+  p.hb = p.tb > 1 ? heads : heads_per_block(blocks, heads, places, sms);
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + p.hb - 1) / p.hb));
   if (grid.y > 65535) return BLASST_EINVAL;
-  const size_t smem = std::max<size_t>(1, a->rot / 2) * sizeof(float2);
+  const size_t smem = static_cast<size_t>(p.tb) * std::max(1, a->rot / 2) * sizeof(float2);
   const cudaStream_t s = static_cast<cudaStream_t>(a->stream);
   if (a->dtype == BLASST_BF16)
     return wide ? launch_append<__nv_bfloat16, 8>(p, grid, smem, s)
