@@ -45,6 +45,8 @@ struct SeqBwdParams {
   const uint32_t* norms;     // [Hkv][2]: largest |dO row|^2, |v row|^2 (bits); null: dS is not scaled
   const int* cu_q;
   const int* cu_k;
+  const void* k;
+  long long k_st, k_sh;
   int n_seq, Tq, Tk, Hq, Hkv, g;
   int rt;       // tokens per 128-row tile
   int n_key, n_row;  // most items per KV head
@@ -185,7 +187,9 @@ struct SeqBwdCfg {
   static constexpr int OFF_A = 0;  // what stays: K, V or Q, dO
   static constexpr int OFF_R1 = 2 * TILE;
   static constexpr int OFF_R2 = OFF_R1 + NS1 * TILE;
-  static constexpr int OFF_ST = OFF_R2 + NS2 * TILE;  // [NST][2][128] fp32
+  // key item: [NST][2][128] fp32 statistics; row item: [2][128] what the
+  // roundings of dS lost, [D] a mean of the keys
+  static constexpr int OFF_ST = OFF_R2 + NS2 * TILE;
   static constexpr int OFF_BAR = OFF_ST + NST * 1024;
   static constexpr int B_A = 0;
   static constexpr int B_TAIL = 1;
@@ -590,6 +594,32 @@ __global__ void __launch_bounds__(384, 1)
         if (lane == 0) ptx::mbar_arrive(bar(C::B_STF + slot));
       }
       if (!ok && lane == 0) fail();
+    } else if (warp == C::WARP_ROWS && n > 0) {
+      // ======================= a mean of the keys ============================
+      // over up to 32 keys that every row of the item sees (0 if there are none)
+      const int m = p.causal ? min(it.off + it.at + 1, it.kvlen) : it.kvlen;
+      const int count = max(min(m, 32), 0);
+      constexpr int V = D / 32;
+      float sum[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+      const T* base = static_cast<const T*>(p.k) + static_cast<long long>(it.k0) * p.k_st + it.hk * p.k_sh + lane * V;
+#pragma unroll 8
+      for (int i = 0; i < count; ++i) {
+        const long long row = m <= 32 ? i : (static_cast<long long>(i) * m) >> 5;
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+          float a, b;
+          seq_unpack2<T>(*reinterpret_cast<const uint32_t*>(base + row * p.k_st + v), a, b);
+          sum[v] += a;
+          sum[v + 1] += b;
+        }
+      }
+      float* mean = reinterpret_cast<float*>(smem + C::OFF_ST + 1024);
+#pragma unroll
+      for (int v = 0; v < V; ++v) mean[lane * V + v] = count > 0 ? sum[v] / static_cast<float>(count) : 0.0f;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(C::B_STF));
     }
   } else {
     ptx::reg_take<C::REGS_SOFT>();
@@ -617,6 +647,11 @@ __global__ void __launch_bounds__(384, 1)
         limit = p.causal ? min(it.off + tok + 1, it.kvlen) : it.kvlen;
         least = p.causal ? min(it.off + it.at + 1, it.kvlen) : it.kvlen;
       }
+      // Row item: dQ = scale (sum_j r_ij k_j + (sum_j dS_ij - r_ij) kappa), r = dS
+      // rounded, kappa a mean of the keys. What all keys have in common (often
+      // large) cancels in the exact sum, as sum_j dS_ij is 0 but for o's own
+      // rounding; r's errors do not cancel it and are kept from it this way.
+      float lost = 0.0f;
       float pv[64];
       // the lane's visible columns of tile i: [lo, hi), relative to the warpgroup's
       auto columns = [&](int i, int& lo, int& hi) -> bool {
@@ -714,6 +749,19 @@ __global__ void __launch_bounds__(384, 1)
           ptx::mbar_arrive(bar(C::B_DS + (i & 1)));
           if (key) ptx::mbar_arrive(bar(C::B_STE + i % C::NST));
         }
+        if (!key) {
+          // (while S of the next tile is awaited)
+          float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float r0, r1;
+            seq_unpack2<T>(pk[j], r0, r1);
+            ptx::fma2(r0, r1, r0, r1, -1.0f, -1.0f, pv[2 * j], pv[2 * j + 1]);
+            const int a = 2 * (j & 1);
+            ptx::add2(t[a], t[a + 1], t[a], t[a + 1], r0, r1);
+          }
+          lost += (t[0] + t[1]) + (t[2] + t[3]);
+        }
         return true;
       };
       if (n > 0) ok = form_p(0);
@@ -722,6 +770,16 @@ __global__ void __launch_bounds__(384, 1)
         if (ok && i + 1 < n) ok = form_p(i + 1);
       }
       if (ok && n > 0) ok = warp_wait(bar(C::B_ACC), 0);
+      float common = 0.0f;  // both warpgroups' `lost` of the lane's row
+      const float* mean = reinterpret_cast<const float*>(smem + C::OFF_ST + 1024);
+      if (!key && ok && n > 0) {
+        float* all = reinterpret_cast<float*>(smem + C::OFF_ST);
+        all[wg * 128 + row] = lost;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_STE));
+        ok = warp_wait(bar(C::B_STE), 0) && warp_wait(bar(C::B_STF), 0);
+        if (ok) common = all[row] + all[128 + row];
+      }
       ok = ok && *abort_flag == 0;
       ok = __all_sync(0xffffffffu, ok) != 0;
       if (!ok) {
@@ -748,6 +806,11 @@ __global__ void __launch_bounds__(384, 1)
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) r[j] = 0u;
+          }
+          if (!key && n > 0) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              r[j] = __float_as_uint(fmaf(common, mean[32 * k + j], __uint_as_float(r[j])));
           }
           if (exists) {
             uint4* dst = reinterpret_cast<uint4*>(out + 32 * k);

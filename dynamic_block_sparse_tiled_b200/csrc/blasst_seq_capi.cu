@@ -496,6 +496,9 @@ int blasst_packed_bwd(const blasst_packed_bwd_args* a) {
   p.dv = a->dv;
   p.stats = stats;
   p.norms = f16 ? norms : nullptr;
+  p.k = a->k;
+  p.k_st = a->k_st;
+  p.k_sh = a->k_sh;
   p.cu_q = a->cu_q;
   p.cu_k = a->cu_k;
   p.n_seq = a->n_seq;
