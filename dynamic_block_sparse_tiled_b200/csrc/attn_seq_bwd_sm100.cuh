@@ -49,7 +49,7 @@ struct SeqBwdParams {
   long long k_st, k_sh;
   int n_seq, Tq, Tk, Hq, Hkv, g;
   int rt;       // tokens per 128-row tile
-  int n_key, n_row;  // most items per KV head
+  int n_key, n_row;  // places for items per KV head
   int causal;
   float scale, scale_log2;
   float p_unscale;  // undoes P's shift
@@ -257,55 +257,38 @@ __global__ void __launch_bounds__(384, 1)
     const bool key = static_cast<int>(blockIdx.x) < n_keys;
     const int idx = key ? blockIdx.x : blockIdx.x - n_keys;
     const int per = key ? p.n_key : p.n_row;
-    const int h = idx / per, want = idx % per;
+    const int tile = key ? C::BK : p.rt, tokens = key ? p.Tk : p.Tq;
+    const int* cu = key ? p.cu_k : p.cu_q;
+    // longest first under a causal mask: the first keys, the last rows
+    const int place = key ? idx % per : per - 1 - idx % per;
     // after a wait gave up, calls before blasst_check do nothing
     const bool live = !(p.err && *reinterpret_cast<volatile int*>(p.err) == BLASST_ETIMEOUT);
-    auto span = [&](int s) -> SeqSpan {
-      return seq_span(p.cu_q, p.cu_k, nullptr, 0, p.Tq, p.Tk, p.rt, s, p.err);
-    };
+    const int s = live ? seq_of_place(cu, p.n_seq, tokens, tile, place, lane) : -1;
     SeqBwdItem it{};
-    int before = 0;
-    // longest first under a causal mask: the first keys, the last rows
-    for (int s0 = 0; s0 < p.n_seq && it.kind == 0 && live; s0 += 32) {
-      const int i = s0 + lane;
-      const int s = key ? i : p.n_seq - 1 - i;
-      SeqSpan mine{};
-      if (i < p.n_seq) mine = span(s);
-      const int tiles = key ? (mine.kvlen + C::BK - 1) / C::BK : mine.tiles;
-      int upto = tiles;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += v;
-      }
-      const uint32_t hit = __ballot_sync(0xffffffffu, want < before + upto);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        const int n = __shfl_sync(0xffffffffu, tiles, l);
-        const int start = before + __shfl_sync(0xffffffffu, upto, l) - n;
-        const SeqSpan q = seq_span_of(mine, l);
-        it.hk = h;
+    if (s >= 0) {
+      const SeqSpan q = seq_span(p.cu_q, p.cu_k, nullptr, 0, p.Tq, p.Tk, p.rt, s, p.err);
+      const int t = place - seq_place(cu, s, tokens, tile);
+      if (t < (key ? (q.kvlen + C::BK - 1) / C::BK : q.tiles)) {
+        it.hk = idx / per;
         it.q0 = q.q0;
         it.qlen = q.qlen;
         it.k0 = q.k0;
         it.kvlen = q.kvlen;
         it.off = q.off;
+        it.at = t * tile;
         if (key) {
           it.kind = 1;
-          it.at = (want - start) * C::BK;
           // from the first token that sees a key of the tile: no row without
           // keys is ever streamed
           it.first = p.causal ? min(max(it.at - q.off, 0), q.qlen) : 0;
           it.steps = (q.qlen - it.first + p.rt - 1) / p.rt;
         } else {
           it.kind = 2;
-          it.at = (n - 1 - (want - start)) * p.rt;
           const int last = min(it.at + p.rt, q.qlen) - 1;
           const int keys = p.causal ? min(max(q.off + last + 1, 0), q.kvlen) : q.kvlen;
           it.steps = (keys + C::BK - 1) / C::BK;
         }
       }
-      before += __shfl_sync(0xffffffffu, upto, 31);
     }
     if (lane == 0) {
       itemw[0] = it.kind;

@@ -70,7 +70,7 @@ struct SeqAttnParams {
   int rt;        // tokens per 128-row tile
   int rt_few;    // tokens per 32 rows (0: a group is larger)
   int it_tok;    // tokens per item: rt (the kernel for few rows) or 2 rt
-  int n_tiles;   // most tiles per KV head (one item per CTA); 0: shared list
+  int n_tiles;   // places for items per KV head (one item per CTA); 0: shared list
   int causal;
   float scale_log2;
   float* part_o;    // [2 * grid][256][D]
@@ -125,6 +125,30 @@ __device__ __forceinline__ SeqSpan seq_span_of(const SeqSpan& q, int l) {
   r.off = r.kvlen - r.qlen;
   r.tiles = __shfl_sync(0xffffffffu, q.tiles, l);
   return r;
+}
+
+// Place of a sequence's first tile among `tokens / tile + n_seq` places: every
+// sequence has enough of them behind it for its tiles, whatever the lengths,
+// and a place's sequence is found without looking at all of them.
+__device__ __forceinline__ int seq_place(const int* cu, int s, int tokens, int tile) {
+  return static_cast<int>(static_cast<uint32_t>(min(max(cu[s], 0), tokens)) / static_cast<uint32_t>(tile)) + s;
+}
+
+// The last sequence whose first place is at or before `place` (-1: none), by
+// the warp, 32 probes at a time.
+__device__ __forceinline__ int seq_of_place(const int* cu, int n_seq, int tokens, int tile, int place,
+                                            int lane) {
+  int lo = 0, hi = n_seq;
+  for (;;) {
+    const int step = (hi - lo + 31) >> 5;
+    const int i = lo + lane * step;
+    const uint32_t at = __ballot_sync(0xffffffffu, i < hi && seq_place(cu, min(i, n_seq - 1), tokens, tile) <= place);
+    const int k = __popc(at);
+    if (k == 0) return -1;
+    lo += (k - 1) * step;
+    hi = min(hi, lo + step);
+    if (step == 1) return lo;
+  }
 }
 
 template <int D, bool FEW>
@@ -324,9 +348,9 @@ __device__ __forceinline__ void seq_few_take(const float* x, T* o, float* part) 
   }
 }
 
-template <int ST>
-struct SeqStream {
-  static constexpr int value = ST;
+template <int N>
+struct SeqInt {
+  static constexpr int value = N;
 };
 
 template <int D, typename T, bool FEW>
@@ -455,172 +479,201 @@ __global__ void __launch_bounds__(384, 1)
     const bool live = !(p.err && *reinterpret_cast<volatile int*>(p.err) == BLASST_ETIMEOUT);
     bool ok = true;
     if (p.n_tiles != 0) {
-      // ---- one item, counted from the last tile of the last sequence -------
+      // ---- one item: the last tiles of a head first ------------------------
       const int h = static_cast<int>(blockIdx.x) / p.n_tiles;
-      const int want = static_cast<int>(blockIdx.x) % p.n_tiles;
-      int before = 0;
-      bool found = false;
-      for (int s0 = p.n_seq - 1; s0 >= 0 && !found && live; s0 -= 32) {
-        const SeqSpan mine = span(s0 - lane);
-        int upto = mine.tiles;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, upto, d);
-          if (lane >= d) upto += v;
+      const int place = p.n_tiles - 1 - static_cast<int>(blockIdx.x) % p.n_tiles;
+      const int s = live ? seq_of_place(p.cu_q, p.n_seq, p.Tq, p.it_tok, place, lane) : -1;
+      if (s >= 0) {
+        const SeqSpan q = span(s);
+        const int t = place - seq_place(p.cu_q, s, p.Tq, p.it_tok);
+        if (t < q.tiles) {
+          const SeqItem it = seq_item(q, p.causal, p.rt, p.it_tok, t);
+          ok = put(s, q, h, it, 0, it.nblk);
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, want < before + upto);
-        if (hit) {
-          const int l = __ffs(hit) - 1;
-          const int end = before + __shfl_sync(0xffffffffu, upto, l);
-          const SeqSpan q = seq_span_of(mine, l);
-          const SeqItem it = seq_item(q, p.causal, p.rt, p.it_tok, end - 1 - want);
-          ok = put(s0 - l, q, h, it, 0, it.nblk);
-          found = true;
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
       }
     } else {
       // ---- this CTA's range of the shared list -----------------------------
       // no item cut at the range's end, until one is found
       if (lane == 0) p.part_desc[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
-      // the sequences' spans are read 32 at a time, one per lane; up to 32 of
-      // them are read once
-      int chunk = -1;
-      SeqSpan mine;
-      auto load_chunk = [&](int s0) {
-        if (s0 == chunk) return;
-        mine = span(s0 + lane);
-        chunk = s0;
-      };
-      auto span_of = [&](int s) -> SeqSpan {
-        load_chunk(s & ~31);
-        return seq_span_of(mine, s & 31);
-      };
-      long long total = 0, items = 0, blocks = 0, own = 0;
-      auto add_up = [&](long long c) -> long long {
+      // the sequences' spans are read 32 U at a time, U per lane; up to that
+      // many are read once (one per lane while that is enough: four took 6 us
+      // more of a call with three sequences)
+      auto my_part = [&](auto per_lane) {
+        constexpr int U = decltype(per_lane)::value, CHUNK = 32 * U;
+        int chunk = -1;
+        SeqSpan mine[U];
+        auto load_chunk = [&](int s0) {
+          if (s0 == chunk) return;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
-        return c;
-      };
-      for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
-        load_chunk(s0);
-        const SeqCost c = seq_cost(mine, p.causal, p.rt, p.it_tok);
-        own = c.cost * p.Hkv;
-        total += add_up(own);
-        items += add_up(c.items) * p.Hkv;
-        blocks += add_up(c.blocks) * p.Hkv;
-      }
-      // Little work (an eighth of a CTA's worth of items to spare, few blocks
-      // each): every CTA one piece of one item, so that none has to start
-      // another item behind its first.
-      const long long spare = static_cast<long long>(gridDim.x) - items;
-      const long long piece = spare > 0 ? max(2ll, seq_div(blocks + spare - 1, spare)) : 0;
-      const bool little = 8 * spare >= gridDim.x && piece <= kSeqMostPiece;
-      if (little) {
-        const int r = static_cast<int>(piece);
-        long long at = 0;
-        for (int s0 = 0; s0 < p.n_seq && live; s0 += 32) {
+          for (int u = 0; u < U; ++u) mine[u] = span(s0 + lane * U + u);
+          chunk = s0;
+        };
+        auto span_of = [&](int s) -> SeqSpan {
+          load_chunk(s & ~(CHUNK - 1));
+          SeqSpan r = mine[0];
+#pragma unroll
+          for (int u = 1; u < U; ++u)
+            if ((s & (U - 1)) == u) r = mine[u];
+          return seq_span_of(r, (s & (CHUNK - 1)) / U);
+        };
+        long long total = 0, items = 0, blocks = 0, own = 0;
+        auto add_up = [&](long long c) -> long long {
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
+          return c;
+        };
+        auto lane_cost = [&]() -> long long {
+          long long c = 0;
+#pragma unroll
+          for (int u = 0; u < U; ++u) c += seq_cost(mine[u], p.causal, p.rt, p.it_tok).cost;
+          return c * p.Hkv;
+        };
+        for (int s0 = 0; s0 < p.n_seq; s0 += CHUNK) {
           load_chunk(s0);
-          long long np = 0;
-          for (int t = 0; t < mine.tiles; ++t)
-            np += seq_pieces(seq_item(mine, p.causal, p.rt, p.it_tok, t), r);
-          long long upto = np * p.Hkv;
+          SeqCost c{0, 0, 0};
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const SeqCost one = seq_cost(mine[u], p.causal, p.rt, p.it_tok);
+            c.cost += one.cost;
+            c.items += one.items;
+            c.blocks += one.blocks;
+          }
+          own = c.cost * p.Hkv;
+          total += add_up(own);
+          items += add_up(c.items) * p.Hkv;
+          blocks += add_up(c.blocks) * p.Hkv;
+        }
+        // Little work (an eighth of a CTA's worth of items to spare, few blocks
+        // each): every CTA one piece of one item, so that none has to start
+        // another item behind its first.
+        const long long spare = static_cast<long long>(gridDim.x) - items;
+        const long long piece = spare > 0 ? max(2ll, seq_div(blocks + spare - 1, spare)) : 0;
+        const bool little = 8 * spare >= gridDim.x && piece <= kSeqMostPiece;
+        if (little) {
+          const int r = static_cast<int>(piece);
+          long long at = 0;
+          auto pieces_of = [&](const SeqSpan& q) -> long long {
+            long long n_pieces = 0;
+            for (int t = 0; t < q.tiles; ++t)
+              n_pieces += seq_pieces(seq_item(q, p.causal, p.rt, p.it_tok, t), r);
+            return n_pieces;
+          };
+          for (int s0 = 0; s0 < p.n_seq && live; s0 += CHUNK) {
+            load_chunk(s0);
+            long long np = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) np += pieces_of(mine[u]) * p.Hkv;
+            long long upto = np;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+              const long long v = __shfl_up_sync(0xffffffffu, upto, d);
+              if (lane >= d) upto += v;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, blockIdx.x < at + upto);
+            if (hit) {
+              const int l = __ffs(hit) - 1;
+              at += __shfl_sync(0xffffffffu, upto - np, l);
+              int s = s0 + l * U;  // one of the lane's sequences
+              SeqSpan q = span_of(s);
+              long long per = pieces_of(q);
+              while (blockIdx.x >= at + per * p.Hkv) {
+                at += per * p.Hkv;
+                q = span_of(++s);
+                per = pieces_of(q);
+              }
+              int left = static_cast<int>(blockIdx.x - at);
+              const int h = left / static_cast<int>(per);
+              left -= h * static_cast<int>(per);
+              SeqItem it = seq_item(q, p.causal, p.rt, p.it_tok, 0);
+              int n_pieces = seq_pieces(it, r);
+              for (int t = 1; left >= n_pieces; ++t) {
+                left -= n_pieces;
+                it = seq_item(q, p.causal, p.rt, p.it_tok, t);
+                n_pieces = seq_pieces(it, r);
+              }
+              if (lane == 0 && left == 0 && n_pieces > 1) {
+                p.part_desc[2 * blockIdx.x] = make_int4(q.q0 + it.tok0, it.ntok, h, it.one ? 1 : 0);
+                p.part_desc[2 * blockIdx.x + 1] = make_int4(blockIdx.x + n_pieces - 1, 0, 0, 0);
+              }
+              ok = put(s, q, h, it, left * r, min(left * r + r, it.nblk));
+              break;
+            }
+            at += __shfl_sync(0xffffffffu, upto, 31);
+          }
+        }
+        const long long share = seq_div(total + gridDim.x - 1, gridDim.x);
+        const long long range = share < kSeqMinRange ? kSeqMinRange : share;
+        const long long lo = range * blockIdx.x;
+        const long long hi = lo + range < total ? lo + range : total;
+        long long at = 0;  // the list's place of what is looked at
+        int s = 0, h = 0, t = 0;
+        bool found = false;
+        for (int s0 = 0; s0 < p.n_seq && !found && !little && live && lo < total; s0 += CHUNK) {
+          if (s0 != chunk) {
+            load_chunk(s0);
+            own = lane_cost();
+          }
+          long long upto = own;
 #pragma unroll
           for (int d = 1; d < 32; d <<= 1) {
             const long long v = __shfl_up_sync(0xffffffffu, upto, d);
             if (lane >= d) upto += v;
           }
-          const uint32_t hit = __ballot_sync(0xffffffffu, blockIdx.x < at + upto);
+          const uint32_t hit = __ballot_sync(0xffffffffu, lo < at + upto);
           if (hit) {
             const int l = __ffs(hit) - 1;
-            np = __shfl_sync(0xffffffffu, np, l);
-            int left = static_cast<int>(blockIdx.x - (at + __shfl_sync(0xffffffffu, upto, l) - np * p.Hkv));
-            const int h = left / static_cast<int>(np);
-            left -= h * static_cast<int>(np);
-            const SeqSpan q = seq_span_of(mine, l);
-            SeqItem it = seq_item(q, p.causal, p.rt, p.it_tok, 0);
-            int n_pieces = seq_pieces(it, r);
-            for (int t = 1; left >= n_pieces; ++t) {
-              left -= n_pieces;
-              it = seq_item(q, p.causal, p.rt, p.it_tok, t);
-              n_pieces = seq_pieces(it, r);
+            at += __shfl_sync(0xffffffffu, upto - own, l);
+            s = s0 + l * U;  // one of the lane's sequences
+            long long per = seq_cost(span_of(s), p.causal, p.rt, p.it_tok).cost;
+            while (lo >= at + per * p.Hkv) {
+              at += per * p.Hkv;
+              per = seq_cost(span_of(++s), p.causal, p.rt, p.it_tok).cost;
             }
-            if (lane == 0 && left == 0 && n_pieces > 1) {
-              p.part_desc[2 * blockIdx.x] = make_int4(q.q0 + it.tok0, it.ntok, h, it.one ? 1 : 0);
-              p.part_desc[2 * blockIdx.x + 1] = make_int4(blockIdx.x + n_pieces - 1, 0, 0, 0);
-            }
-            ok = put(s0 + l, q, h, it, left * r, min(left * r + r, it.nblk));
-            break;
+            h = static_cast<int>(seq_div(lo - at, per));
+            at += h * per;
+            found = true;
+          } else {
+            at += __shfl_sync(0xffffffffu, upto, 31);
           }
-          at += __shfl_sync(0xffffffffu, upto, 31);
         }
-      }
-      const long long share = seq_div(total + gridDim.x - 1, gridDim.x);
-      const long long range = share < kSeqMinRange ? kSeqMinRange : share;
-      const long long lo = range * blockIdx.x;
-      const long long hi = lo + range < total ? lo + range : total;
-      long long at = 0;  // the list's place of what is looked at
-      int s = 0, h = 0, t = 0;
-      bool found = false;
-      for (int s0 = 0; s0 < p.n_seq && !found && !little && live && lo < total; s0 += 32) {
-        if (s0 != chunk) {
-          load_chunk(s0);
-          own = seq_cost(mine, p.causal, p.rt, p.it_tok).cost * p.Hkv;
-        }
-        long long upto = own;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const long long v = __shfl_up_sync(0xffffffffu, upto, d);
-          if (lane >= d) upto += v;
-        }
-        const uint32_t hit = __ballot_sync(0xffffffffu, lo < at + upto);
-        if (hit) {
-          const int l = __ffs(hit) - 1;
-          at += __shfl_sync(0xffffffffu, upto - own, l);
-          const long long per_head = seq_div(__shfl_sync(0xffffffffu, own, l), p.Hkv);
-          s = s0 + l;
-          h = static_cast<int>(seq_div(lo - at, per_head));
-          at += h * per_head;
-          found = true;
-        } else {
-          at += __shfl_sync(0xffffffffu, upto, 31);
-        }
-      }
-      if (found) {
-        SeqSpan q = span_of(s);
-        while (at < hi && ok) {
-          const SeqItem it = seq_item(q, p.causal, p.rt, p.it_tok, t);
-          const long long end = at + kSeqItemCost + static_cast<long long>(it.nblk) * it.unit;
-          if (end > lo) {
-            const int b0 = it.nblk ? seq_first_block(at, it, lo) : 0;
-            const int b1 = it.nblk ? seq_first_block(at, it, hi) : 0;
-            // (an item that begins before the range and has no block that
-            // starts in it is the range before's)
-            if (at >= lo || b0 < b1) {
-              if (lane == 0 && b0 == 0 && b1 < it.nblk) {
-                // it goes on in the ranges behind this one: what the join needs
-                p.part_desc[2 * blockIdx.x] =
-                    make_int4(q.q0 + it.tok0, it.ntok, h, it.one ? 1 : 0);
-                p.part_desc[2 * blockIdx.x + 1] =
-                    make_int4(static_cast<int>(seq_div(end - it.unit, range)), 0, 0, 0);
+        if (found) {
+          SeqSpan q = span_of(s);
+          while (at < hi && ok) {
+            const SeqItem it = seq_item(q, p.causal, p.rt, p.it_tok, t);
+            const long long end = at + kSeqItemCost + static_cast<long long>(it.nblk) * it.unit;
+            if (end > lo) {
+              const int b0 = it.nblk ? seq_first_block(at, it, lo) : 0;
+              const int b1 = it.nblk ? seq_first_block(at, it, hi) : 0;
+              // (an item that begins before the range and has no block that
+              // starts in it is the range before's)
+              if (at >= lo || b0 < b1) {
+                if (lane == 0 && b0 == 0 && b1 < it.nblk) {
+                  // it goes on in the ranges behind this one: what the join needs
+                  p.part_desc[2 * blockIdx.x] =
+                      make_int4(q.q0 + it.tok0, it.ntok, h, it.one ? 1 : 0);
+                  p.part_desc[2 * blockIdx.x + 1] =
+                      make_int4(static_cast<int>(seq_div(end - it.unit, range)), 0, 0, 0);
+                }
+                ok = put(s, q, h, it, b0, b1);
               }
-              ok = put(s, q, h, it, b0, b1);
             }
-          }
-          at = end;
-          if (++t == q.tiles) {
-            t = 0;
-            if (++h == p.Hkv) {
-              h = 0;
-              do {
-                if (++s >= p.n_seq) break;
-                q = span_of(s);
-              } while (q.tiles == 0);
-              if (s >= p.n_seq) break;
+            at = end;
+            if (++t == q.tiles) {
+              t = 0;
+              if (++h == p.Hkv) {
+                h = 0;
+                do {
+                  if (++s >= p.n_seq) break;
+                  q = span_of(s);
+                } while (q.tiles == 0);
+                if (s >= p.n_seq) break;
+              }
             }
           }
         }
-      }
+      };
+      if (p.n_seq <= 32) my_part(SeqInt<1>{});
+      else my_part(SeqInt<4>{});
     }
     if (ok) {
       SeqSpan q{};
@@ -864,8 +917,8 @@ __global__ void __launch_bounds__(384, 1)
           return true;
         };
         // two tiles: stream 1 sees every block, stream 0 the first cnt0 of them
-        const SeqStream<0> s0;
-        const SeqStream<1> s1;
+        const SeqInt<0> s0;
+        const SeqInt<1> s1;
         if (cnt0 > 0) ok = issue_s(s0, true, one);
         if (ok && cnt1 > 0) ok = issue_s(s1, one || cnt0 == 0, true);
         // O is free once the item before has been read out

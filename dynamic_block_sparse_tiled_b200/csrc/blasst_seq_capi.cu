@@ -136,7 +136,7 @@ int run_seq(blasst::SeqAttnParams& p, const void* q, long long q_st, long long q
   const bool few = p.rt_few > 0 && static_cast<long long>(p.Tq) * p.g <= 32ll * p.n_seq;
   p.it_tok = few ? p.rt : 2 * p.rt;
   const long long full = static_cast<long long>(p.Tq) / p.it_tok;
-  const long long tiles = std::min<long long>(p.Tq, full + p.n_seq);
+  const long long tiles = full + p.n_seq;  // places (seq_place)
   const bool single = full * p.Hkv >= 8ll * sms || most_keys <= kSeqFewKeys;
   p.n_tiles = single && tiles * p.Hkv < 0x7fffffffll ? static_cast<int>(tiles) : 0;
   const size_t rows = static_cast<size_t>(sms) * 2 * 256;
@@ -480,9 +480,9 @@ int blasst_packed_bwd(const blasst_packed_bwd_args* a) {
   blasst::SeqBwdParams p{};
   p.g = a->Hq / a->Hkv;
   p.rt = 128 / p.g;
-  // most tiles a KV head can have, whatever the lengths
-  const long long n_key = std::min<long long>(a->Tk, a->Tk / 128 + static_cast<long long>(a->n_seq));
-  const long long n_row = std::min<long long>(a->Tq, a->Tq / p.rt + static_cast<long long>(a->n_seq));
+  // places for tiles (seq_place)
+  const long long n_key = a->Tk > 0 ? a->Tk / 128 + static_cast<long long>(a->n_seq) : 0;
+  const long long n_row = a->Tq > 0 ? a->Tq / p.rt + static_cast<long long>(a->n_seq) : 0;
   if ((n_key + n_row) * a->Hkv > 0x7fffffffll) return BLASST_EINVAL;
   p.n_key = static_cast<int>(n_key);
   p.n_row = static_cast<int>(n_row);

@@ -43,13 +43,21 @@ int dtype_of(const Tensor& t) {
   }
 }
 
-// The device of a call: its first tensor's. The rest is checked against it.
+// The device of a call, its first tensor's (the rest is checked against it),
+// and its stream, current while the call allocates.
 class Call {
  public:
-  explicit Call(const Tensor& first) {
+  Call(const Tensor& first, const Stream& given) {
     if (!first.is_cuda()) refuse("tensors passed to the CUDA library must live on a CUDA device");
     device_ = first.get_device();
     guard_.set_index(device_);
+    const auto now = c10::cuda::getCurrentCUDAStream(device_);
+    raw_ = now.stream();
+    if (given && reinterpret_cast<cudaStream_t>(*given) != raw_) {
+      raw_ = reinterpret_cast<cudaStream_t>(*given);
+      caller_ = now.unwrap();
+      stream_guard_.reset_stream(c10::cuda::getStreamFromExternal(raw_, device_).unwrap());
+    }
   }
   // A float tensor of `dims` dimensions, contiguous in the last.
   const Tensor& rows(const Tensor& t, const char* name, int dims) const {
@@ -94,25 +102,19 @@ class Call {
     p = w.data_ptr();
     n = w.nbytes();
   }
-  // A tensor allocated here: handed to the call's stream by stream().
+  // A tensor allocated here, for the call's stream; the caller's own may use it too.
   Tensor made(Tensor t) {
-    made_[n_made_++] = t;
+    if (caller_) t.record_stream(*caller_);
     return t;
   }
-  void* stream(const Stream& given) const {
-    if (!given) return c10::cuda::getCurrentCUDAStream(device_).stream();
-    cudaStream_t raw = reinterpret_cast<cudaStream_t>(*given);
-    // allocated for the current stream, used on this one
-    for (int i = 0; i < n_made_; ++i)
-      made_[i].record_stream(c10::cuda::getStreamFromExternal(raw, device_).unwrap());
-    return raw;
-  }
+  void* stream() const { return raw_; }
 
  private:
   c10::cuda::OptionalCUDAGuard guard_;
+  c10::cuda::OptionalCUDAStreamGuard stream_guard_;
+  std::optional<c10::Stream> caller_;
+  cudaStream_t raw_ = nullptr;
   c10::DeviceIndex device_ = 0;
-  Tensor made_[4];
-  int n_made_ = 0;
 };
 
 int same_dtype(const Tensor& t, std::initializer_list<const Tensor*> others) {
@@ -164,7 +166,7 @@ void pages(const Call& c, Args& a, const Tensor& k, const Tensor& v, const Tenso
 
 Tensor rotary(const Tensor& x, const Tensor& inv_freq, const Maybe& positions, bool interleaved,
               double mscale, const Maybe& out, const Stream& stream, bool inverse) {
-  Call c(x);
+  Call c(x, stream);
   const bool packed = x.dim() == 3;
   c.rows(x, "x", packed ? 3 : 4);
   const Tensor y = out ? c.rows(*out, "out", static_cast<int>(x.dim()))
@@ -199,7 +201,7 @@ Tensor rotary(const Tensor& x, const Tensor& inv_freq, const Maybe& positions, b
   a.interleaved = interleaved;
   a.inverse = inverse;
   a.scale = static_cast<float>(mscale);
-  a.stream = c.stream(stream);
+  a.stream = c.stream();
   if (x.numel() > 0) check(blasst_rotary(&a), "blasst_rotary");
   return y;
 }
@@ -208,7 +210,7 @@ Tensor paged_append(const Tensor& q, const Tensor& k, const Tensor& v, const Ten
                     const Tensor& v_pages, const Tensor& table, const Tensor& kv_lens,
                     const Tensor& cu_q, const Maybe& inv_freq, bool interleaved, double mscale,
                     const Maybe& q_out, const Stream& stream) {
-  Call c(q);
+  Call c(q, stream);
   c.rows(q, "q", 3);
   c.rows(k, "k", 3);
   c.rows(v, "v", 3);
@@ -237,7 +239,7 @@ Tensor paged_append(const Tensor& q, const Tensor& k, const Tensor& v, const Ten
   if (inv_freq) a.freq = c.frequencies(*inv_freq, a.rot);
   a.interleaved = interleaved;
   a.scale = static_cast<float>(mscale);
-  a.stream = c.stream(stream);
+  a.stream = c.stream();
   if (a.T > 0) check(blasst_append(&a), "blasst_append");
   return o;
 }
@@ -269,7 +271,7 @@ void packed(Call& c, Args& a, const Tensor& q, const Tensor& k, const Tensor& v,
 std::pair<Tensor, Tensor> attention_packed(const Tensor& q, const Tensor& k, const Tensor& v,
                                            const Tensor& cu_q, const Maybe& cu_k, bool causal,
                                            double scale, const Maybe& workspace, const Stream& stream) {
-  Call c(q);
+  Call c(q, stream);
   blasst_packed_args a{};
   packed(c, a, q, k, v, cu_q, cu_k);
   a.dtype = same_dtype(q, {&k, &v});
@@ -280,7 +282,7 @@ std::pair<Tensor, Tensor> attention_packed(const Tensor& q, const Tensor& k, con
   a.causal = causal;
   a.scale = static_cast<float>(scale);
   c.workspace(workspace, blasst_seq_workspace_bytes(a.d), q, a.workspace, a.workspace_bytes);
-  a.stream = c.stream(stream);
+  a.stream = c.stream();
   if (a.Tq > 0) check(blasst_packed_fwd(&a), "blasst_packed_fwd");
   return {o, lse};
 }
@@ -289,7 +291,7 @@ std::tuple<Tensor, Tensor, Tensor> attention_packed_backward(
     const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& o, const Tensor& lse,
     const Tensor& dout, const Tensor& cu_q, const Maybe& cu_k, bool causal, double scale,
     const Maybe& workspace, const Stream& stream) {
-  Call c(q);
+  Call c(q, stream);
   blasst_packed_bwd_args a{};
   packed(c, a, q, k, v, cu_q, cu_k);
   c.rows(o, "o", 3);
@@ -315,7 +317,7 @@ std::tuple<Tensor, Tensor, Tensor> attention_packed_backward(
   a.scale = static_cast<float>(scale);
   c.workspace(workspace, blasst_packed_bwd_workspace_bytes(a.Tq, a.Hq, a.Hkv), q, a.workspace,
               a.workspace_bytes);
-  a.stream = c.stream(stream);
+  a.stream = c.stream();
   if (a.Tq > 0 || a.Tk > 0) check(blasst_packed_bwd(&a), "blasst_packed_bwd");
   return {dq, dk, dv};
 }
@@ -324,7 +326,7 @@ std::pair<Tensor, Tensor> attention_paged(const Tensor& q, const Tensor& k_pages
                                           const Tensor& table, const Tensor& kv_lens,
                                           const Tensor& cu_q, bool causal, double scale,
                                           const Maybe& workspace, const Stream& stream) {
-  Call c(q);
+  Call c(q, stream);
   c.rows(q, "q", 3);
   blasst_paged_args a{};
   pages(c, a, k_pages, v_pages, table, kv_lens, cu_q);
@@ -345,7 +347,7 @@ std::pair<Tensor, Tensor> attention_paged(const Tensor& q, const Tensor& k_pages
   a.causal = causal;
   a.scale = static_cast<float>(scale);
   c.workspace(workspace, blasst_seq_workspace_bytes(a.d), q, a.workspace, a.workspace_bytes);
-  a.stream = c.stream(stream);
+  a.stream = c.stream();
   if (a.Tq > 0) check(blasst_paged_fwd(&a), "blasst_paged_fwd");
   return {o, lse};
 }

@@ -226,6 +226,53 @@ def test_packed_and_gradients(bl, dtype, q_lens, k_lens, hq, hkv, d, causal):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("first", [0, 333])
+def test_many_sequences(bl, first):
+    """More sequences than one look of a warp covers, empty ones among them, through
+    both ways of dealing out the work (few keys in all, and many)."""
+    import torch
+    g = gen(20)
+    n = 1500
+    q_lens = [(0, 1, 2, 7, 1, 0, 40)[i % 7] for i in range(n)]
+    for k_lens in (q_lens, [(3 * i) % 25 for i in range(n)], [1 + (i == 700) * 3000 for i in range(n)]):
+        t, tk = sum(q_lens) + first, sum(k_lens) + first
+        q, k, v = rand(g, t, 2, 64, dtype="bfloat16"), rand(g, tk, 1, 64, dtype="bfloat16"), rand(g, tk, 1, 64, dtype="bfloat16")
+        cq, ck = R.cu(q_lens, first), R.cu(k_lens, first)
+        o, lse = bl.attention_packed(q, k, v, cq, ck)
+        dout = rand(g, t, 2, 64, dtype="bfloat16")
+        got = bl.attention_packed_backward(q, k, v, o, lse, dout, cq, ck)
+        assert bl.blasst_check() == 0
+        own = slice(first, None)
+        R.check_packed((o[own], lse[own]), q[own], k[own], v[own], q_lens, k_lens, True)
+        R.check_grads([x[own] for x in got], q[own], k[own], v[own], o[own], lse[own], dout[own], q_lens, k_lens, True)
+    kv_lens = [1 + (37 * i) % 90 + (i % 97 == 5) * 1500 for i in range(700)]
+    ones = [1 + (i % 50 == 3) for i in range(700)]
+    kp, vp, table, rows = R.paged(kv_lens, 16, 1, 64, torch.float16, g)
+    q = rand(g, sum(ones), 4, 64, dtype="float16")
+    got = bl.attention_paged(q, kp, vp, table, torch.tensor(kv_lens, dtype=torch.int32, device="cuda"), R.cu(ones))
+    assert bl.blasst_check() == 0
+    k, v = (torch.cat([r[i] for r in rows]) for i in range(2))
+    R.check_packed(got, q, k, v, ones, kv_lens, True)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_side_without_tokens(bl, dtype):
+    import torch
+    q, k, v, g = qkv(21, [5, 9], [5, 9], 4, 2, 64, dtype)
+    cu, none = R.cu([5, 9]), R.cu([0, 0])
+    o, lse = bl.attention_packed(q, k[:0], v[:0], cu, none)
+    assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+    got = bl.attention_packed_backward(q, k[:0], v[:0], o, lse, torch.ones_like(q), cu, none)
+    assert bool((got[0] == 0).all()) and got[1].shape == (0, 2, 64)
+    o, lse = bl.attention_packed(q[:0], k, v, none, cu)
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    got = bl.attention_packed_backward(q[:0], k, v, o, lse, q[:0], none, cu)
+    assert bool((got[1] == 0).all()) and bool((got[2] == 0).all())
+    o, lse = bl.attention_packed(q, k, v, cu[:1])  # no sequence at all
+    assert o.shape == q.shape
+    assert bl.blasst_check() == 0
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_packed_strides_scale_and_unowned_tokens(bl, dtype):
     """One projection's q, k and v side by side, tokens before the first and behind
