@@ -23,8 +23,18 @@
 //                dQ += dS K                   (A from TMEM)
 // Warps 0-7 form P and dS (thread = TMEM lane, warpgroup w = columns
 // [64 w, 64 w + 64)); warp 8: TMA producer; warp 9: tcgen05 issuer; warp 10:
-// finds the item, then (key item) brings the rows' statistics. P and dS go
-// back to TMEM as 16-bit pairs, each warpgroup's over its own columns.
+// finds the item, then brings the rows' statistics (key item) or a mean of the
+// keys (row item). P and dS go back to TMEM as 16-bit pairs, each warpgroup's
+// over its own columns.
+//
+// Rounding: P and dS to the inputs' type before their products, the outputs
+// once; all sums and statistics in fp32.
+//
+// What bounds it: the tensor core with its issue, 80 cycles per 128 x 128 x 16
+// product (cuBLAS takes about 84); a key item's step takes about 3700 cycles
+// for 2560 of products, waiting for P's 128 x 128 exponentials (1024 cycles of
+// MUFU), a row item's about 2600 for 1920. 16384 tokens in 5 sequences, 32 / 8
+// heads of 128, bf16, causal: 2.43 ms, 0.76 PFLOP/s counting five products.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>

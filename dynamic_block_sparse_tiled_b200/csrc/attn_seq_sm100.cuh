@@ -38,9 +38,20 @@
 // Work: either one item (sequence, KV head, tile) per CTA, the last tiles of
 // a head first (enough tiles to fill the GPU several times), or a resident
 // grid that cuts the list of all key blocks of all items into equal ranges
-// ("shared list"): an item cut by a range's end leaves fp32 partials, joined
-// by seq_join_kernel in the order of the ranges, so results do not depend on
-// timing.
+// ("shared list"), or, where that list is short, gives every CTA one piece of
+// one item: an item cut by a range's or piece's end leaves fp32 partials,
+// joined by seq_join_kernel in their order, so results do not depend on timing.
+//
+// Rounding: scores, the softmax's statistics, O and partials are fp32; P is
+// rounded to the inputs' type, which the tensor core takes next to V, and o
+// once at the end.
+//
+// What bounds it. Long prompts: the tensor core with its issue, about 95 cycles
+// per 128 x 128 x 16 product beside the softmax's TMEM traffic (64 ideal; 32768
+// prompt tokens of 32 / 8 heads of 128, bf16: 2.95 ms, 1.06 PFLOP/s). Single
+// tokens: memory (16 x 65536 cached tokens of 8 KV heads of 128: 645-680 us,
+// 0.97 of a copy's rate). Short calls: latency (511 tokens in 5 prompts: 12 us
+// on the GPU, 2 of set-up, 1.5 to find the item, 1.5 for the first loads).
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -154,8 +165,7 @@ __device__ __forceinline__ int seq_of_place(const int* cu, int n_seq, int tokens
 template <int D, bool FEW>
 struct SeqAttnCfg {
   static constexpr int NTHREADS = 384;
-  // registers per thread: a softmax thread keeps its 128 scores; 2 x 216 + 72
-  // = 3 x 168, what the launch has
+  // registers per thread: 2 x 200 + 104 = 3 x 168, what the launch has
   static constexpr int REGS = 168, REGS_SOFT = 200, REGS_REST = 104;
   static constexpr int NSOFT = 256;
   static constexpr int WARP_K = 8, WARP_MMA = 9, WARP_ITEM = 10, WARP_V = 11;
