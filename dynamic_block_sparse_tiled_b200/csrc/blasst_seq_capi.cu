@@ -388,7 +388,7 @@ int blasst_append(const blasst_append_args* a) {
   const int heads = (a->q ? a->Hq : 0) + 2 * a->Hkv;
   const int groups = std::max(1, 256 / std::min(places, 256));
   p.tb = 1;
-  while (2 * p.tb <= std::min(groups, blasst::kAppendTokens) && a->T >= 8ll * p.tb * sms) p.tb *= 2;
+  while (2 * p.tb <= std::min(groups, blasst::kAppendTokens) && a->T >= 4ll * p.tb * sms) p.tb *= 2;
   const int blocks = (a->T + p.tb - 1) / p.tb;
   p.hb = p.tb > 1 ? heads : heads_per_block(blocks, heads, places, sms);
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + p.hb - 1) / p.hb));
