@@ -23,7 +23,7 @@
 //                dQ += dS K                   (A from TMEM)
 // Warps 0-7 form P and dS (thread = TMEM lane, warpgroup w = columns
 // [64 w, 64 w + 64)); warp 8: TMA producer; warp 9: tcgen05 issuer; warp 10:
-// finds the item, then brings the rows' statistics (key item) or a mean of the
+// finds the item, then brings the rows' statistics (key item) or means of the
 // keys (row item). P and dS go back to TMEM as 16-bit pairs, each warpgroup's
 // over its own columns.
 //
@@ -198,9 +198,11 @@ struct SeqBwdCfg {
   static constexpr int OFF_R1 = 2 * TILE;
   static constexpr int OFF_R2 = OFF_R1 + NS1 * TILE;
   // key item: [NST][2][128] fp32 statistics; row item: [2][128] what the
-  // roundings of dS lost, [D] a mean of the keys
+  // roundings of dS lost, [3][D] means of the keys
   static constexpr int OFF_ST = OFF_R2 + NS2 * TILE;
-  static constexpr int OFF_BAR = OFF_ST + NST * 1024;
+  static constexpr int ST_BYTES = 1024 + (3 * D * 4 > 1024 ? 3 * D * 4 : 1024);
+  static_assert(ST_BYTES >= NST * 1024, "statistics' slots");
+  static constexpr int OFF_BAR = OFF_ST + ST_BYTES;
   static constexpr int B_A = 0;
   static constexpr int B_TAIL = 1;
   static constexpr int B_F1 = 2;
@@ -588,29 +590,69 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (!ok && lane == 0) fail();
     } else if (warp == C::WARP_ROWS && n > 0) {
-      // ======================= a mean of the keys ============================
-      // over up to 32 keys that every row of the item sees (0 if there are none)
+      // ======================= means of the keys =============================
+      // Of up to 32 keys that every row of the item sees; at a sequence's start,
+      // where the first row sees few, also of the first 4 and 16 for the rows
+      // that see those. Each is drawn towards 0 by what a mean of so few is off
+      // (Stein: by V / n of |mean|^2, V the keys' variance); of one key nothing
+      // is known (taken for the mean it made dQ of 40 causal tokens worse than
+      // without any: error 2.8e-3 where two roundings make 2.4e-3).
       const int m = p.causal ? min(it.off + it.at + 1, it.kvlen) : it.kvlen;
-      const int count = max(min(m, 32), 0);
-      constexpr int V = D / 32;
-      float sum[V];
+      const int most = p.causal ? min(it.off + min(it.at + p.rt, it.qlen), it.kvlen) : it.kvlen;
+      // four columns per lane, and of d = 64 two keys at a time
+      constexpr int LPK = D / 4, KP = 32 / LPK;
+      const int sub = lane / LPK, col = lane % LPK * 4;
+      const T* base = static_cast<const T*>(p.k) + static_cast<long long>(it.k0) * p.k_st + it.hk * p.k_sh + col;
+      // `count` keys, evenly over the first `over`
+      auto mean_of = [&](int level, int count, int over) {
+        float sum[4] = {0.f, 0.f, 0.f, 0.f}, squares = 0.0f, of_mean = 0.0f;
+#pragma unroll 1
+        for (int i0 = sub; i0 < count; i0 += 4 * KP) {
+          uint2 w[4];
 #pragma unroll
-      for (int v = 0; v < V; ++v) sum[v] = 0.0f;
-      const T* base = static_cast<const T*>(p.k) + static_cast<long long>(it.k0) * p.k_st + it.hk * p.k_sh + lane * V;
-#pragma unroll 8
-      for (int i = 0; i < count; ++i) {
-        const long long row = m <= 32 ? i : (static_cast<long long>(i) * m) >> 5;
+          for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * KP;
+            const T* at = base + (over <= 32 ? i : (static_cast<long long>(i) * over) >> 5) * p.k_st;
+            w[j] = i < count ? *reinterpret_cast<const uint2*>(at) : make_uint2(0u, 0u);
+          }
 #pragma unroll
-        for (int v = 0; v < V; v += 2) {
-          float a, b;
-          seq_unpack2<T>(*reinterpret_cast<const uint32_t*>(base + row * p.k_st + v), a, b);
-          sum[v] += a;
-          sum[v + 1] += b;
+          for (int j = 0; j < 4; ++j) {
+            float x[4];
+            seq_unpack2<T>(w[j].x, x[0], x[1]);
+            seq_unpack2<T>(w[j].y, x[2], x[3]);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              sum[v] += x[v];
+              squares = fmaf(x[v], x[v], squares);
+            }
+          }
         }
-      }
-      float* mean = reinterpret_cast<float*>(smem + C::OFF_ST + 1024);
+        __syncwarp();
+        const float keys = static_cast<float>(max(count, 2));
 #pragma unroll
-      for (int v = 0; v < V; ++v) mean[lane * V + v] = count > 0 ? sum[v] / static_cast<float>(count) : 0.0f;
+        for (int v = 0; v < 4; ++v) {
+          if (KP == 2) sum[v] += __shfl_xor_sync(0xffffffffu, sum[v], 16);
+          sum[v] /= keys;
+          of_mean = fmaf(sum[v], sum[v], of_mean);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+          squares += __shfl_xor_sync(0xffffffffu, squares, d);
+          of_mean += __shfl_xor_sync(0xffffffffu, of_mean, d);
+        }
+        of_mean /= static_cast<float>(KP);
+        const float variance = fmaxf(squares - keys * of_mean, 0.0f) / (keys - 1.0f);
+        const float part = count > 1 && of_mean > 0.0f ? fmaxf(1.0f - variance / (keys * of_mean), 0.0f) : 0.0f;
+        if (sub == 0)
+          *reinterpret_cast<float4*>(smem + C::OFF_ST + 1024 + (level * D + col) * 4) =
+              part > 0.0f ? make_float4(sum[0] * part, sum[1] * part, sum[2] * part, sum[3] * part)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+      };
+#pragma unroll 1
+      for (int level = 0; level < 3; ++level) {
+        const int count = level == 0 ? max(min(m, 32), 0) : level == 1 ? 4 : 16;
+        if (level == 0 || (m < count && count <= most)) mean_of(level, count, level == 0 ? m : count);
+      }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(C::B_STF));
     }
@@ -626,6 +668,7 @@ __global__ void __launch_bounds__(384, 1)
       const uint32_t s_tm = tmem + lane_base + C::S_COL + wg * 64;
       const float sl2 = p.scale_log2;
       bool ok = true;
+      volatile float* all = reinterpret_cast<volatile float*>(smem + C::OFF_ST);
       // row item: the lane's token and statistics
       const int tok = it.at + row / p.g;
       const bool exists = key ? it.at + row < it.kvlen : row < box_rows && tok < it.qlen;
@@ -639,6 +682,9 @@ __global__ void __launch_bounds__(384, 1)
         }
         limit = p.causal ? min(it.off + tok + 1, it.kvlen) : it.kvlen;
         least = p.causal ? min(it.off + it.at + 1, it.kvlen) : it.kvlen;
+        // the mean of the most keys that the lane's row sees for certain; kept in
+        // shared memory meanwhile (the loop has no register to spare)
+        all[wg * 128 + row] = least < 16 && limit >= 16 ? 2.0f : least < 4 && limit >= 4 ? 1.0f : 0.0f;
       }
       // Row item: dQ = scale (sum_j r_ij k_j + (sum_j dS_ij - r_ij) kappa), r = dS
       // rounded, kappa a mean of the keys. What all keys have in common (often
@@ -766,7 +812,7 @@ __global__ void __launch_bounds__(384, 1)
       float common = 0.0f;  // both warpgroups' `lost` of the lane's row
       const float* mean = reinterpret_cast<const float*>(smem + C::OFF_ST + 1024);
       if (!key && ok && n > 0) {
-        float* all = reinterpret_cast<float*>(smem + C::OFF_ST);
+        mean += static_cast<int>(all[wg * 128 + row]) * D;
         all[wg * 128 + row] = lost;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(C::B_STE));
