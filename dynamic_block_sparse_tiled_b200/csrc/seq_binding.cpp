@@ -56,7 +56,8 @@ class Call {
     if (given && reinterpret_cast<cudaStream_t>(*given) != raw_) {
       raw_ = reinterpret_cast<cudaStream_t>(*given);
       caller_ = now.unwrap();
-      stream_guard_.reset_stream(c10::cuda::getStreamFromExternal(raw_, device_).unwrap());
+      given_ = c10::cuda::getStreamFromExternal(raw_, device_).unwrap();
+      stream_guard_.reset_stream(*given_);
     }
   }
   // A float tensor of `dims` dimensions, contiguous in the last.
@@ -67,8 +68,11 @@ class Call {
       refuse(std::string(name) + " must be contiguous in its last dimension");
     return t;
   }
+  // (on a stream of the caller's choice, a tensor that is freed behind the call
+  // stays until the kernel has read it)
   void here(const Tensor& t) const {
     if (!t.is_cuda() || t.get_device() != device_) refuse("tensors must live on one CUDA device");
+    if (given_) t.record_stream(*given_);
   }
   const int* index(const Tensor& t, const char* name, long long n) const {
     here(t);
@@ -112,7 +116,7 @@ class Call {
  private:
   c10::cuda::OptionalCUDAGuard guard_;
   c10::cuda::OptionalCUDAStreamGuard stream_guard_;
-  std::optional<c10::Stream> caller_;
+  std::optional<c10::Stream> caller_, given_;  // set if the call's stream is not the current one
   cudaStream_t raw_ = nullptr;
   c10::DeviceIndex device_ = 0;
 };

@@ -597,6 +597,25 @@ def test_streams_and_own_workspaces(bl):
     assert bl.blasst_check() == 0
 
 
+def test_inputs_freed_behind_a_call_on_another_stream(bl):
+    """A tensor that the caller drops after a call on a stream of its choice is not
+    given to anyone else before the kernel has read it."""
+    import torch
+    side = torch.cuda.Stream()
+    freq, _ = bl.rope_frequencies(128)
+    x = rand(gen(29), 1000, 8, 128, dtype="bfloat16")
+    want = bl.rotary(x, freq)
+    mine = x.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+    y = bl.rotary(mine, freq, stream=side)
+    del mine
+    others = [torch.full_like(x, 7.0) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and len(others) == 4
+
+
 def test_captured_steps_follow_the_lengths(bl):
     """A decode step captured once and replayed with longer sequences and other
     pages; a captured training step replayed with other inputs."""
