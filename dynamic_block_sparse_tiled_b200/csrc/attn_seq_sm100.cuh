@@ -35,8 +35,11 @@
 // 16-bit pairs over the first 64 of the same columns once S is in registers),
 // O0, O1.
 //
-// Work: either one item (sequence, KV head, tile) per CTA, the last tiles of
-// a head first (enough tiles to fill the GPU several times), or a resident
+// Work: either whole items (sequence, KV head, tile), the last tiles of a head
+// first (enough tiles to fill the GPU several times), which a resident grid
+// takes one after the other from a list, so that one's output and the next
+// one's loads overlap (32768 prompt tokens: 2.84 -> 2.74 ms over a CTA per
+// item; results do not depend on who takes which); or a resident
 // grid that cuts the list of all key blocks of all items into equal ranges
 // ("shared list"), or, where that list is short, gives every CTA one piece of
 // one item: an item cut by a range's or piece's end leaves fp32 partials,
@@ -48,7 +51,7 @@
 //
 // What bounds it. Long prompts: the tensor core with its issue, about 95 cycles
 // per 128 x 128 x 16 product beside the softmax's TMEM traffic (64 ideal; 32768
-// prompt tokens of 32 / 8 heads of 128, bf16: 2.95 ms, 1.06 PFLOP/s). Single
+// prompt tokens of 32 / 8 heads of 128, bf16: 2.74 ms, 1.14 PFLOP/s). Single
 // tokens: memory (16 x 65536 cached tokens of 8 KV heads of 128: 645-680 us,
 // 0.97 of a copy's rate). Short calls: latency (511 tokens in 5 prompts: 12 us
 // on the GPU, 2 of set-up, 1.5 to find the item, 1.5 for the first loads).
@@ -81,7 +84,8 @@ struct SeqAttnParams {
   int rt;        // tokens per 128-row tile
   int rt_few;    // tokens per 32 rows (0: a group is larger)
   int it_tok;    // tokens per item: rt (the kernel for few rows) or 2 rt
-  int n_tiles;   // places for items per KV head (one item per CTA); 0: shared list
+  int n_tiles;   // places for items per KV head (whole items); 0: shared list
+  int* next;     // whole items: how many the CTAs took behind their first; null: one item per CTA
   int causal;
   float scale_log2;
   float* part_o;    // [2 * grid][256][D]
@@ -199,7 +203,8 @@ struct SeqAttnCfg {
   static constexpr int NITEM = 2;
   static constexpr int B_IF = B_DRAIN + 1;   // [NITEM] item record written
   static constexpr int B_IE = B_IF + NITEM;  // [NITEM] read (2 loaders, issuer, 8 softmax warps)
-  static constexpr int NBAR = B_IE + NITEM;
+  static constexpr int B_NEXT = B_IE + NITEM;  // the item's last K block is on its way
+  static constexpr int NBAR = B_NEXT + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   // misc words: [0] tmem base, [1] abort, [3] always 0
   static constexpr int MISC_BYTES = 16;
@@ -407,12 +412,36 @@ __global__ void __launch_bounds__(384, 1)
     ptx::mbar_init(bar(C::B_ML), 8);
     ptx::mbar_init(bar(C::B_X), 8);
     ptx::mbar_init(bar(C::B_DRAIN), 1);
+    ptx::mbar_init(bar(C::B_NEXT), 1);
     for (int i = 1; i < 4; ++i) misc[i] = 0;
     ptx::fence_mbar_init();
   }
   if (warp == C::WARP_MMA) {
     ptx::tmem_alloc(ptx::smem_u32(const_cast<int*>(misc)), C::TMEM_COLS);
     ptx::tmem_relinquish();
+  }
+  auto span = [&](int s) -> SeqSpan {
+    if (s < 0 || s >= p.n_seq) return SeqSpan{};
+    const int kv_cap = static_cast<int>(
+        min(static_cast<long long>(p.table_width) * p.page_size, 0x7fffff00ll));
+    return seq_span(p.cu_q, p.cu_k, p.kv_lens, kv_cap, p.Tq, p.Tk, p.it_tok, s, p.err);
+  };
+  // whole item i, the last tiles of a head first: its sequence (-1: none) and tile
+  auto find = [&](int i, SeqSpan& q, int& t) -> int {
+    const int place = p.n_tiles - 1 - i % p.n_tiles;
+    const int s = seq_of_place(p.cu_q, p.n_seq, p.Tq, p.it_tok, place, lane);
+    if (s < 0) return -1;
+    q = span(s);
+    t = place - seq_place(p.cu_q, s, p.Tq, p.it_tok);
+    return t < q.tiles ? s : -1;
+  };
+  // beside the set-up: the CTA's first whole item, or the lane's sequence of the
+  // shared list
+  SeqSpan first_q{};
+  int first_s = -1, first_t = 0;
+  if (warp == C::WARP_ITEM) {
+    if (p.n_tiles != 0) first_s = find(static_cast<int>(blockIdx.x), first_q, first_t);
+    else first_q = span(lane);
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -450,12 +479,6 @@ __global__ void __launch_bounds__(384, 1)
    ptx::reg_give<C::REGS_REST>();
    if (warp == C::WARP_ITEM) {
     // ======================= the CTA's items ================================
-    const int kv_cap = static_cast<int>(
-        min(static_cast<long long>(p.table_width) * p.page_size, 0x7fffff00ll));
-    auto span = [&](int s) -> SeqSpan {
-      if (s < 0 || s >= p.n_seq) return SeqSpan{};
-      return seq_span(p.cu_q, p.cu_k, p.kv_lens, kv_cap, p.Tq, p.Tk, p.it_tok, s, p.err);
-    };
     int n = 0;
     auto put = [&](int s, const SeqSpan& q, int h, const SeqItem& it, int b0, int b1) -> bool {
       const int slot = n % C::NITEM;
@@ -489,17 +512,26 @@ __global__ void __launch_bounds__(384, 1)
     const bool live = !(p.err && *reinterpret_cast<volatile int*>(p.err) == BLASST_ETIMEOUT);
     bool ok = true;
     if (p.n_tiles != 0) {
-      // ---- one item: the last tiles of a head first ------------------------
-      const int h = static_cast<int>(blockIdx.x) / p.n_tiles;
-      const int place = p.n_tiles - 1 - static_cast<int>(blockIdx.x) % p.n_tiles;
-      const int s = live ? seq_of_place(p.cu_q, p.n_seq, p.Tq, p.it_tok, place, lane) : -1;
-      if (s >= 0) {
-        const SeqSpan q = span(s);
-        const int t = place - seq_place(p.cu_q, s, p.Tq, p.it_tok);
-        if (t < q.tiles) {
+      // ---- whole items -----------------------------------------------------
+      // One, or the CTA's first and then one after the other from the list of
+      // all, each taken when the one before has its last K block on its way
+      // (sooner would leave the list's end less even, later K's ring empty).
+      const int count = p.n_tiles * p.Hkv;
+      int i = static_cast<int>(blockIdx.x);
+      SeqSpan q = first_q;
+      int s = first_s, t = first_t;
+      while (live && i < count) {
+        if (s >= 0) {
           const SeqItem it = seq_item(q, p.causal, p.rt, p.it_tok, t);
-          ok = put(s, q, h, it, 0, it.nblk);
+          ok = put(s, q, i / p.n_tiles, it, 0, it.nblk);
+          if (ok && p.next) ok = ptx::mbar_wait(bar(C::B_NEXT), (n - 1) & 1, abort_flag, p.timeout_ns);
+          ok = __all_sync(0xffffffffu, ok) != 0;
+          if (!ok) break;
         }
+        if (!p.next) break;
+        if (lane == 0) i = static_cast<int>(gridDim.x) + atomicAdd(p.next, 1);
+        i = __shfl_sync(0xffffffffu, i, 0);
+        if (i < count) s = find(i, q, t);
       }
     } else {
       // ---- this CTA's range of the shared list -----------------------------
@@ -510,8 +542,9 @@ __global__ void __launch_bounds__(384, 1)
       // more of a call with three sequences)
       auto my_part = [&](auto per_lane) {
         constexpr int U = decltype(per_lane)::value, CHUNK = 32 * U;
-        int chunk = -1;
+        int chunk = U == 1 ? 0 : -1;
         SeqSpan mine[U];
+        mine[0] = first_q;
         auto load_chunk = [&](int s0) {
           if (s0 == chunk) return;
 #pragma unroll
@@ -771,7 +804,10 @@ __global__ void __launch_bounds__(384, 1)
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
           few_before = it.few();
         }
-        if (b == nb || !ok) break;
+        if (b == nb || !ok) {
+          if (!is_v && ok && lane == 0) ptx::mbar_arrive(bar(C::B_NEXT));
+          break;
+        }
         const int key0 = (it.b0 + b) * C::BK;
         const int valid = min(C::BK, it.kvlen - key0);
         // this lane's piece of the block

@@ -106,7 +106,11 @@ int launch_seq(const CUtensorMap& mq, const CUtensorMap& mq_few, const CUtensorM
   if (e != cudaSuccess) return cuda_status(e);
   const bool shared_list = p.n_tiles == 0;
   const unsigned grid =
-      shared_list ? static_cast<unsigned>(sms) : static_cast<unsigned>(p.n_tiles) * p.Hkv;
+      shared_list || p.next ? static_cast<unsigned>(sms) : static_cast<unsigned>(p.n_tiles) * p.Hkv;
+  if (p.next) {
+    e = cudaMemsetAsync(p.next, 0, sizeof(int), stream);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
   kernel<<<grid, C::NTHREADS, C::SMEM_BYTES, stream>>>(mq, mq_few, mk, mv, p);
   int rc = cuda_status(cudaGetLastError());
   if (rc != BLASST_OK || !shared_list) return rc;
@@ -139,6 +143,10 @@ int run_seq(blasst::SeqAttnParams& p, const void* q, long long q_st, long long q
   const long long tiles = full + p.n_seq;  // places (seq_place)
   const bool single = full * p.Hkv >= 8ll * sms || most_keys <= kSeqFewKeys;
   p.n_tiles = single && tiles * p.Hkv < 0x7fffffffll ? static_cast<int>(tiles) : 0;
+  // Several whole items per SM: a resident grid takes them from a list, so that an
+  // item's end and the next one's loads overlap (a CTA of its own cost each item
+  // about 4 us of set-up; the list costs its clearing, 2 us).
+  p.next = p.n_tiles != 0 && static_cast<long long>(p.n_tiles) * p.Hkv > 2ll * sms ? static_cast<int*>(workspace) : nullptr;
   const size_t rows = static_cast<size_t>(sms) * 2 * 256;
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = p.part_o + rows * d;
