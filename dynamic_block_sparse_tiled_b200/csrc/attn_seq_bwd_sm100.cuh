@@ -34,7 +34,7 @@
 // product (cuBLAS takes about 84); a key item's step takes about 3700 cycles
 // for 2560 of products, waiting for P's 128 x 128 exponentials (1024 cycles of
 // MUFU), a row item's about 2600 for 1920. 16384 tokens in 5 sequences, 32 / 8
-// heads of 128, bf16, causal: 2.43 ms, 0.76 PFLOP/s counting five products.
+// heads of 128, bf16, causal: 2.42 ms, 0.76 PFLOP/s counting five products.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
