@@ -101,8 +101,10 @@ struct SeqSpan {
   int q0, qlen, k0, kvlen, off, tiles;
 };
 
+// `err`: the two device error words. An index error has one of its own: it must
+// neither stop other calls, as a wait that gave up does, nor hide one.
 __device__ __forceinline__ void seq_record_error(int* err, int code) {
-  if (err) atomicCAS(err, 0, code);
+  if (err) atomicCAS(code == BLASST_EINDEX ? err + 1 : err, 0, code);
 }
 
 __device__ __forceinline__ SeqSpan seq_span(const int* cu_q, const int* cu_k, const int* kv_lens,

@@ -26,9 +26,11 @@
 
 namespace {
 
-// Device error word: set (first error wins) by kernels whose bounded waits
-// gave up; read and cleared by blasst_check().
-__device__ int g_blasst_error = 0;
+// Device error words, read and cleared by blasst_check(). [0]: set (first error
+// wins) by kernels whose bounded waits gave up; while it is set, kernels that
+// start do not compute. [1]: an index error of the operators over sequences,
+// which concerns the affected sequences only and stops nobody.
+__device__ int g_blasst_error[2] = {0, 0};
 
 constexpr int kMaxDevices = 64;
 using blasst::capi::kTimeoutNs;
@@ -43,7 +45,7 @@ int current_device() {
   return dev;
 }
 
-// Address of the error word on the current device (looked up once per device).
+// Address of the error words on the current device (looked up once per device).
 int* error_word() {
   const int dev = current_device();
   if (dev < 0 || dev >= kMaxDevices) return nullptr;
@@ -745,15 +747,15 @@ int blasst_check(void* stream) {
   if (cudaStreamSynchronize(s) != cudaSuccess) return BLASST_ECUDA;
   int* err = error_word();
   if (!err) return BLASST_ECUDA;
-  int host = 0;
-  if (cudaMemcpy(&host, err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
+  int host[2] = {0, 0};
+  if (cudaMemcpy(host, err, sizeof(host), cudaMemcpyDeviceToHost) != cudaSuccess)
     return BLASST_ECUDA;
-  if (host != 0) {
-    const int zero = 0;
-    if (cudaMemcpy(err, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
+  if (host[0] != 0 || host[1] != 0) {
+    const int zero[2] = {0, 0};
+    if (cudaMemcpy(err, zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
       return BLASST_ECUDA;
   }
-  return host;
+  return host[0] != 0 ? host[0] : host[1];
 }
 
 }  // extern "C"

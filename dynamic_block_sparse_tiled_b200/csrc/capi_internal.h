@@ -12,7 +12,8 @@ namespace capi {
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per bounded wait
 
-// The device error word's address on the current device, or null.
+// The address of the two device error words (waits that gave up, index errors)
+// on the current device, or null.
 int* error_word();
 // cuTensorMapEncodeTiled, or null.
 PFN_cuTensorMapEncodeTiled_v12000 encoder();

@@ -533,11 +533,14 @@ BLASST_API int blasst_paged_fwd(const blasst_paged_args* args);
 BLASST_API size_t blasst_seq_workspace_bytes(int d);
 
 /* Synchronises `stream`, then returns (and clears) the device error word:
- * BLASST_OK, BLASST_ETIMEOUT if a kernel's bounded wait gave up, or
- * BLASST_ECUDA if the stream reported a CUDA error. While the word holds an
- * error, prefill CTAs that start return without computing (so a failing
- * launch ends within one wave of bounded waits) and decode merges write NaN:
- * outputs of calls made after an error and before this check are undefined. */
+ * BLASST_OK, BLASST_ETIMEOUT if a kernel's bounded wait gave up,
+ * BLASST_EINDEX if an operator over sequences met a length, offset or page
+ * number out of range (ETIMEOUT is returned if both happened), or
+ * BLASST_ECUDA if the stream reported a CUDA error. After a wait gave up,
+ * prefill CTAs that start return without computing (so a failing launch ends
+ * within one wave of bounded waits) and decode merges write NaN: outputs of
+ * calls made after it and before this check are undefined. After an index
+ * error only the affected sequences' outputs are; other calls compute. */
 BLASST_API int blasst_check(void* stream);
 
 /* Self-test of the two exponentials the prefill kernel uses, so that a test
