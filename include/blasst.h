@@ -433,6 +433,8 @@ BLASST_API int blasst_append(const blasst_append_args* args);
 /* Attention over packed sequences, exact: query token i of sequence s sees
  * key j when j <= i + (len_k - len_q) (causal = 1, bottom-right) or every key
  * of the sequence (causal = 0). Rows without keys get o = 0, lse = -inf.
+ * The weights are rounded to the inputs' type before they meet the values
+ * (fp16: with an absolute error of at most 2^-32 of the row's largest weight).
  *   q [Tq, Hq, d], k, v [Tk, Hkv, d] by strides; o [Tq, Hq, d] and lse
  *   [Tq, Hq] (fp32, natural log) contiguous.
  *   cu_q, cu_k  device int32 [n_seq + 1].
