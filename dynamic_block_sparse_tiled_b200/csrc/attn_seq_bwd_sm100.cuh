@@ -67,13 +67,14 @@ struct SeqBwdParams {
   uint64_t timeout_ns;
 };
 
-// fp16 only: P is kept as 2^8 P, so that the P of long rows (1 / keys) stay
-// normal numbers, and dS as 2^k dS with k from the largest rows of dO and v:
-// |dS| <= 2 |dO_i| |v_j|, so 2^k dS < 2^15 never overflows and uses the whole
+// fp16 only: P (at most 1, but for the rounding of lse) is kept as 2^14 P, so that
+// small P keep all their bits down to 2^-28 (dv of a key that only small weights
+// touch is made of them), and dS as 2^k dS with k from the largest rows of dO and
+// v: |dS| <= 2 |dO_i| |v_j|, so 2^k dS < 2^15 never overflows and uses the whole
 // range. Powers of two, undone in 32 bits at the end.
 template <typename T>
 constexpr float seq_bwd_p_shift() {
-  return SeqType<T>::kFormat == 0 ? 8.0f : 0.0f;
+  return SeqType<T>::kFormat == 0 ? 14.0f : 0.0f;
 }
 
 struct SeqBwdRowsParams {

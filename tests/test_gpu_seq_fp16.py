@@ -130,3 +130,81 @@ def test_references_that_move(bl, step, rows):
         got = bl.attention_packed(q, k, v, R.cu([rows]), R.cu([600]), causal=causal)
         assert bl.blasst_check() == 0
         R.check_packed(got, q, k, v, [rows], [600], causal)
+
+
+# ---------------------------------------------------------------- gradients
+def grads_fp16(q, k, v, o, lse, dout, causal):
+    """One sequence's (dq, dk, dv) in 64 bits with their bounds, and with P and dS
+    and the results rounded as fp16 has them.
+
+    As in seq_ref, but what is under fp16's normal numbers is counted as it is:
+    P is kept as 2^14 P, so it is off by 2^-11 of itself or 2^-39; dS as 2^k dS with
+    2^14 / 2 < 2^k N <= 2^14 for N >= |dO| |v| (of the row for dQ, of all rows for
+    dK; N is found to 2^-8), so it is off by 2^-11 of itself or 2^-25 2^-13 N; the
+    results by 2^-11 of themselves or 2^-25."""
+    import torch
+    n, hq, d = q.shape
+    m, hkv = k.shape[0], k.shape[1]
+    g, scale = hq // hkv, 1 / math.sqrt(d)
+    qq, oo, go = (t.double().transpose(0, 1) for t in (q, o, dout))
+    kk, vv = (R.heads(t, g).transpose(0, 1) for t in (k, v))
+    p = torch.exp(scale * qq @ kk.transpose(1, 2) - lse.double().t()[..., None])
+    if causal:
+        p = p.masked_fill(torch.ones(n, m, dtype=torch.bool, device="cuda").triu(1 + m - n), 0.0)
+    ds = p * (go @ vv.transpose(1, 2) - (go * oo).sum(-1, keepdim=True))
+    a_ds = p * (go.abs() @ vv.abs().transpose(1, 2) + (go * oo).abs().sum(-1, keepdim=True))
+    e = d * 2.0 ** -23 * scale * float((qq.abs() @ kk.abs().transpose(1, 2)).max()) + 2.0 ** -20
+    fold = lambda t: t.reshape(hkv, g, m, d).sum(1).transpose(0, 1)  # noqa: E731
+    big = lambda t: t.norm(dim=-1)  # noqa: E731
+    of_v = big(v.double()).amax(0).repeat_interleave(g)  # per query head
+    of_do = big(go)                                      # [hq, n]
+    of_do_all = of_do.amax(1).view(hkv, g).amax(1).repeat_interleave(g)
+    row, key = 2.0 ** -38 * 1.01 * of_do * of_v[:, None], 2.0 ** -38 * 1.01 * of_do_all * of_v
+    u = 2.0 ** -11
+    want = [scale * (ds @ kk).transpose(0, 1), scale * fold(ds.transpose(1, 2) @ qq), fold(p.transpose(1, 2) @ go)]
+    bound = [scale * ((2 * u + 4 * e) * (a_ds @ kk.abs()) + row[..., None] * kk.abs().sum(1, keepdim=True)).transpose(0, 1),
+             scale * fold((2 * u + 4 * e) * (a_ds.transpose(1, 2) @ qq.abs()) + (key[:, None] * qq.abs().sum(1))[:, None]),
+             fold((2 * u + 2 * e) * (p.transpose(1, 2) @ go.abs()) + 2.0 ** -39 * go.abs().sum(1, keepdim=True))]
+
+    def kept(x, size):
+        """x rounded as fp16 holds 2^k x, 2^14 / 2 < 2^k size <= 2^14."""
+        k2 = torch.exp2(14 - torch.ceil(torch.log2(size.clamp(min=1e-300))))
+        return (x * k2).half().double() / k2
+
+    p16 = kept(p, torch.ones((), dtype=torch.float64, device="cuda"))
+    dq16, dk16 = kept(ds, (of_do * of_v[:, None])[..., None]), kept(ds, (of_do_all * of_v)[:, None, None])
+    # (what dS's roundings lose in a row is not in dQ: seen at its largest where keys have much in common)
+    model = [scale * (dq16 @ kk).transpose(0, 1), scale * fold(dk16.transpose(1, 2) @ qq), fold(p16.transpose(1, 2) @ go)]
+    return want, [b + 2.0 ** -25 for b in bound], [t.half().double() for t in model]
+
+
+def check_fp16(got, q, k, v, o, lse, dout, q_lens, k_lens, causal, what=""):
+    """Every element within its bound; and each sequence's errors, relative to the
+    gradient of their token and head (a few large ones would hide the others), have
+    the model's norm, with 1.25 for its spread."""
+    import torch
+    for i, ((a, b), (c, e)) in enumerate(zip(R.spans(q_lens), R.spans(k_lens))):
+        want, bound, model = grads_fp16(q[a:b], k[c:e], v[c:e], o[a:b], lse[a:b], dout[a:b], causal)
+        for name, t, (x, y), w, bd, md in zip(("dq", "dk", "dv"), got, ((a, b), (c, e), (c, e)), want, bound, model):
+            R.within(t[x:y], w, bd, f"{what} sequence {i} {name}")
+            size = w.norm(dim=-1, keepdim=True)
+            size = torch.where(size == 0, 1.0, size)
+            off, most = float(((t[x:y].double() - w) / size).norm()), float(((md - w) / size).norm())
+            assert off <= 1.25 * most, f"{what} sequence {i} {name}: {off / most:.3g} times the model's error"
+
+
+@pytest.mark.parametrize("over", [14, 16, 18])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+def test_gradients_of_small_weights(bl, over, d, causal):
+    """Values that only small weights touch: their gradients are sums of those."""
+    import torch
+    g = gen(43)
+    lens = [1500, 700]
+    q, k, v = with_sink(g, lens, lens, 4, 2, d, over, "first")
+    dout = (256 * torch.randn(sum(lens), 4, d, generator=g, device="cuda")).half()
+    cu = R.cu(lens)
+    o, lse = bl.attention_packed(q, k, v, cu, causal=causal)
+    got = bl.attention_packed_backward(q, k, v, o, lse, dout, cu, causal=causal)
+    assert bl.blasst_check() == 0
+    check_fp16(got, q, k, v, o, lse, dout, lens, lens, causal)
