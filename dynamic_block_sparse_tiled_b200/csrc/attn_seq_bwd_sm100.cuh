@@ -51,8 +51,10 @@ struct SeqBwdParams {
   void* dq;  // [Tq, Hq, D]
   void* dk;  // [Tk, Hkv, D]
   void* dv;  // [Tk, Hkv, D]
-  const float2* stats;       // [Hkv][Tq][g]: (-lse log2 e + P's shift, D)
-  const uint32_t* norms;     // [Hkv][2]: largest |dO row|^2, |v row|^2 (bits); null: dS is not scaled
+  const float2* stats;    // bf16: [Hkv][Tq][g] (-lse log2 e, D)
+  const float* dsum;      // fp16: [Hkv][Tq][g] D,
+  const uint32_t* sizes;  // [Hkv][Tq][g] sizes for dS' scale (SeqBwdScale),
+  const float* lse;       // [Tq, Hq]
   const int* cu_q;
   const int* cu_k;
   const void* k;
@@ -62,19 +64,54 @@ struct SeqBwdParams {
   int n_key, n_row;  // places for items per KV head
   int causal;
   float scale, scale_log2;
-  float p_unscale;  // undoes P's shift
   int* err;
   uint64_t timeout_ns;
 };
 
 // fp16 only: P (at most 1, but for the rounding of lse) is kept as 2^14 P, so that
 // small P keep all their bits down to 2^-28 (dv of a key that only small weights
-// touch is made of them), and dS as 2^k dS with k from the largest rows of dO and
-// v: |dS| <= 2 |dO_i| |v_j|, so 2^k dS < 2^15 never overflows and uses the whole
-// range. Powers of two, undone in 32 bits at the end.
+// touch is made of them), and dS as 2^k dS: |dS| <= 2 |dO_i| |v_j|, so with k from
+// the largest rows of dO and v 2^k dS < 2^15 never overflows and uses the whole
+// range. The largest are those of what is summed: for dQ the row of dO itself and
+// the sequence's rows of v, for dK the sequence's rows of dO that see the keys. No
+// other sequence has a part in it, nor has a large row in another row's dQ. Powers
+// of two, undone in 32 bits at the end.
+//
+// A size is the upper half of |row|^2 as fp32, rounded up; 0 for rows that are not
+// finite (their products are not either). sizes[hk][t][h]: the lower 16 bits are
+// the size of the row of dO, the upper 16 of a sequence's first rows those of the
+// largest row of v in a part of its keys (SeqSizeParts). Each is stored once, by one
+// block: nothing to clear, no atomics (an atomic maximum per sequence cost a short
+// call 2.5 us).
 template <typename T>
-constexpr float seq_bwd_p_shift() {
-  return SeqType<T>::kFormat == 0 ? 14.0f : 0.0f;
+struct SeqBwdType {
+  static constexpr bool kScaled = SeqType<T>::kFormat == 0;
+  static constexpr float kShift = kScaled ? 14.0f : 0.0f;
+};
+
+__device__ __forceinline__ uint32_t seq_size(float squares) {
+  return squares < INFINITY ? (__float_as_uint(squares) + 0xffffu) >> 16 : 0u;
+}
+
+// k of 2^k dS from two sizes.
+__device__ __forceinline__ int seq_ds_shift(uint32_t a, uint32_t b) {
+  const float n = sqrtf(__uint_as_float(a << 16)) * sqrtf(__uint_as_float(b << 16));
+  return n > 0.0f ? 13 - ilogbf(n) : 0;
+}
+
+// Sizes of v: a sequence's keys in parts of 64, or, where those are more than its
+// rows, in as many times 64 as make them no more.
+constexpr int kBwdRowsPerBlock = 64;
+struct SeqSizeParts {
+  int parts, tiles;  // of the sequence; of 64 keys in a part
+};
+__device__ __forceinline__ SeqSizeParts seq_size_parts(int kvlen, int qlen, int g) {
+  const int tiles = (kvlen + kBwdRowsPerBlock - 1) / kBwdRowsPerBlock;
+  const long long rows = static_cast<long long>(qlen) * g;
+  if (tiles <= rows) return {tiles, 1};
+  const int r = static_cast<int>(rows);
+  const int each = (tiles + r - 1) / r;
+  return {(tiles + each - 1) / each, each};
 }
 
 struct SeqBwdRowsParams {
@@ -82,39 +119,83 @@ struct SeqBwdRowsParams {
   const void* dout;
   const void* v;
   const float* lse;  // [Tq, Hq]
-  float2* stats;
-  uint32_t* norms;  // null: not needed
+  float2* stats;     // bf16
+  float* dsum;       // fp16
+  uint32_t* sizes;
   const int* cu_q;
   const int* cu_k;
   long long o_st, o_sh, do_st, do_sh, v_st, v_sh;
   int n_seq, Tq, Tk, Hq, Hkv, g;
   int row_blocks;  // blocks over the query rows; those behind them take v
-  float shift;
 };
 
-constexpr int kBwdRowsPerBlock = 64;
-
-// Row pass: D_i and the scaled lse of every row, laid out so that a tile's
-// rows are contiguous; with `norms` the largest rows of dO and v too. D / 8
-// lanes per row (16 bytes each), every warp all its rows' loads at once.
-// Bound by memory: o and dO read once.
+// Row pass: D_i of every row, with the scaled lse (bf16) or the row's size (fp16,
+// where blocks behind those of the rows take the parts of v), laid out so that a
+// tile's rows are contiguous. D / 8 lanes per row (16 bytes each), every warp all
+// its rows' loads at once. Bound by memory: o and dO read once.
 template <int D, typename T>
 __global__ void __launch_bounds__(256) blasst_seq_bwd_rows_kernel(const SeqBwdRowsParams p) {
   ptx::grid_launch_dependents();     // (the pair kernel waits before it reads what is written here)
+  constexpr bool SCALED = SeqBwdType<T>::kScaled;
   constexpr int LPR = D / 8;         // lanes per row
   constexpr int RPW = 32 / LPR;      // rows per warp
   constexpr int N = kBwdRowsPerBlock / (8 * RPW);
   const int hk = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPR, at = lane % LPR;
-  const bool of_v = static_cast<int>(blockIdx.x) >= p.row_blocks;
-  const long long block = of_v ? blockIdx.x - p.row_blocks : blockIdx.x;
   const long long all = static_cast<long long>(p.Tq) * p.g;
+  // the sum over a row's lanes, to all of them
+  auto row_sum = [](float x) -> float {
+#pragma unroll
+    for (int d = LPR / 2; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+  };
+  if (SCALED && static_cast<int>(blockIdx.x) >= p.row_blocks) {
+    // ---- a part of v: its largest row ---------------------------------------
+    const int place = static_cast<int>(blockIdx.x) - p.row_blocks;
+    const int s = seq_of_place(p.cu_k, p.n_seq, p.Tk, kBwdRowsPerBlock, place, lane);
+    if (s < 0) return;
+    const SeqSpan q = seq_span(p.cu_q, p.cu_k, nullptr, 0, p.Tq, p.Tk, 1, s, nullptr);
+    const int part = place - seq_place(p.cu_k, s, p.Tk, kBwdRowsPerBlock);
+    if (q.qlen == 0) return;  // no rows: nobody reads it
+    const SeqSizeParts parts = seq_size_parts(q.kvlen, q.qlen, p.g);
+    if (part >= parts.parts) return;
+    const long long keys = static_cast<long long>(parts.tiles) * kBwdRowsPerBlock;
+    const int end = static_cast<int>(min(static_cast<long long>(q.kvlen), (part + 1) * keys));
+    uint32_t most = 0;
+#pragma unroll 4
+    for (int r = static_cast<int>(part * keys) + warp * RPW; r < end; r += 8 * RPW) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (r + sub < end)
+        v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + static_cast<long long>(q.k0 + r + sub) * p.v_st +
+                                            hk * p.v_sh + at * 8);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      float sq0 = 0.0f, sq1 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float a0, a1;
+        seq_unpack2<T>(w[j], a0, a1);
+        ptx::fma2(sq0, sq1, a0, a1, a0, a1, sq0, sq1);
+      }
+      most = max(most, seq_size(row_sum(sq0 + sq1)));
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    __shared__ uint32_t of_warp[8];
+    if (lane == 0) of_warp[warp] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < 8; ++i) most = max(most, of_warp[i]);
+      reinterpret_cast<unsigned short*>(p.sizes + (static_cast<long long>(hk) * p.Tq + q.q0) * p.g + part)[1] =
+          static_cast<unsigned short>(most);
+    }
+    return;
+  }
+  // ---- rows ------------------------------------------------------------------
+  const long long block = blockIdx.x;
   // what belongs to no sequence is not read (it may hold anything)
-  const int* cu = of_v ? p.cu_k : p.cu_q;
-  const uint32_t per = of_v ? 1 : p.g;
-  const long long begin = static_cast<long long>(max(cu[0], 0)) * per;
-  const long long end = static_cast<long long>(min(cu[p.n_seq], of_v ? p.Tk : p.Tq)) * per;
+  const uint32_t per = p.g;
+  const long long begin = static_cast<long long>(max(p.cu_q[0], 0)) * per;
+  const long long end = static_cast<long long>(min(p.cu_q[p.n_seq], p.Tq)) * per;
   uint4 av[N], bv[N];
   float lse[N];
 #pragma unroll
@@ -123,18 +204,13 @@ __global__ void __launch_bounds__(256) blasst_seq_bwd_rows_kernel(const SeqBwdRo
     av[i] = bv[i] = make_uint4(0u, 0u, 0u, 0u);
     lse[i] = 0.0f;
     if (r < begin || r >= end) continue;
-    if (of_v) {
-      av[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + r * p.v_st + hk * p.v_sh + at * 8);
-    } else {
-      // (rows count below 2^38; within a KV head 32 bits hold tokens and heads)
-      const long long t = all >> 32 ? r / per : static_cast<uint32_t>(r) / per;
-      const int h = hk * p.g + static_cast<int>(r - t * per);
-      av[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.dout) + t * p.do_st + h * p.do_sh + at * 8);
-      bv[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.o) + t * p.o_st + h * p.o_sh + at * 8);
-      if (at == 0) lse[i] = p.lse[t * p.Hq + h];
-    }
+    // (rows count below 2^38; within a KV head 32 bits hold tokens and heads)
+    const long long t = all >> 32 ? r / per : static_cast<uint32_t>(r) / per;
+    const int h = hk * p.g + static_cast<int>(r - t * per);
+    av[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.dout) + t * p.do_st + h * p.do_sh + at * 8);
+    bv[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.o) + t * p.o_st + h * p.o_sh + at * 8);
+    if (!SCALED && at == 0) lse[i] = p.lse[t * p.Hq + h];
   }
-  float most = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const long long r = block * kBwdRowsPerBlock + (i * 8 + warp) * RPW + sub;
@@ -147,31 +223,17 @@ __global__ void __launch_bounds__(256) blasst_seq_bwd_rows_kernel(const SeqBwdRo
       seq_unpack2<T>(aw[j], a0, a1);
       seq_unpack2<T>(bw[j], b0, b1);
       ptx::fma2(dot0, dot1, a0, a1, b0, b1, dot0, dot1);
-      if (p.norms) ptx::fma2(sq0, sq1, a0, a1, a0, a1, sq0, sq1);
+      if (SCALED) ptx::fma2(sq0, sq1, a0, a1, a0, a1, sq0, sq1);
     }
-    float dot = dot0 + dot1;
-#pragma unroll
-    for (int d = LPR / 2; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-    if (p.norms) {
-      float sq = sq0 + sq1;
-#pragma unroll
-      for (int d = LPR / 2; d > 0; d >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, d);
-      most = fmaxf(most, sq);
-    }
-    if (at == 0 && !of_v && r >= begin && r < end)
-      p.stats[static_cast<long long>(hk) * all + r] = make_float2(
-          lse[i] == -INFINITY ? -INFINITY : fmaf(lse[i], -1.4426950408889634f, p.shift), dot);
-  }
-  if (p.norms) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-    __shared__ float part[8];
-    if (lane == 0) part[warp] = most;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int i = 1; i < 8; ++i) most = fmaxf(most, part[i]);
-      // a maximum: the order of the blocks does not matter
-      if (most > 0.0f) atomicMax(p.norms + 2 * hk + (of_v ? 1 : 0), __float_as_uint(most));
+    const float dot = row_sum(dot0 + dot1);
+    const uint32_t size = SCALED ? seq_size(row_sum(sq0 + sq1)) : 0u;
+    if (at != 0 || r < begin || r >= end) continue;
+    const long long place = static_cast<long long>(hk) * all + r;
+    if (SCALED) {
+      p.dsum[place] = dot;
+      *reinterpret_cast<unsigned short*>(p.sizes + place) = static_cast<unsigned short>(size);
+    } else {
+      p.stats[place] = make_float2(lse[i] == -INFINITY ? -INFINITY : lse[i] * -1.4426950408889634f, dot);
     }
   }
 }
@@ -222,7 +284,8 @@ struct SeqBwdCfg {
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   // misc words: [0] tmem base, [1] abort, [3] always 0, [4..] the item
   static constexpr int OFF_ITEM = OFF_MISC + 16;
-  static constexpr int SMEM_BYTES = OFF_ITEM + 48;
+  static constexpr int OFF_SIZE = OFF_ITEM + 48;  // [9] largest sizes the warps found
+  static constexpr int SMEM_BYTES = OFF_SIZE + 48;
   static constexpr int S_COL = 0;
   // key item: dP, dV, dK behind S; row item: dQ, then two dP
   static constexpr int K_DP = 128, K_DV = 256, K_DK = 384;
@@ -389,14 +452,47 @@ __global__ void __launch_bounds__(384, 1)
   };
   ptx::grid_wait();  // the rows' statistics (the set-up ran beside their pass)
   // dS = (2^shift P) (c dP - c D) = 2^k P (dP - D)
-  float c = 1.0f, ds_unscale = 1.0f;
-  if (p.norms && n > 0) {
-    const float nm = sqrtf(__uint_as_float(p.norms[2 * it.hk])) *
-                     sqrtf(__uint_as_float(p.norms[2 * it.hk + 1]));
-    const int k = nm > 0.0f && nm < INFINITY ? 14 - (ilogbf(nm) + 1) : 0;
-    c = p.p_unscale * exp2f(static_cast<float>(k));
-    ds_unscale = exp2f(static_cast<float>(-k));
-  }
+  float c = 1.0f;  // (a power of two; 2^-k is taken from it at the end)
+  constexpr bool SCALED = SeqBwdType<T>::kScaled;
+  constexpr float SHIFT = SeqBwdType<T>::kShift;
+  auto seq_row_of = [&]() -> long long { return (static_cast<long long>(it.hk) * p.Tq + it.q0) * p.g; };  // the sequence's first
+  auto set_scale = [&](uint32_t of_do, uint32_t of_v) {
+    c = exp2f(static_cast<float>(seq_ds_shift(of_do, of_v)) - SHIFT);
+  };
+  // the sequence's largest row of v, to all lanes
+  auto size_of_v = [&]() -> uint32_t {
+    const int parts = seq_size_parts(it.kvlen, it.qlen, p.g).parts;
+    uint32_t most = 0;
+    for (int i = lane; i < parts; i += 32) most = max(most, p.sizes[seq_row_of() + i] >> 16);
+    return __reduce_max_sync(0xffffffffu, most);
+  };
+  // key item: from the largest row of dO that is streamed, found by the warps that
+  // need it (0-7, and 10) while the first tiles are on their way: 4 bytes per row
+  // beside the 4 D that the row's streaming takes
+  auto key_scale = [&]() {
+    if (!SCALED || n == 0) return;
+    const int group = warp == C::WARP_ROWS ? 8 : warp;
+    const long long begin = seq_row_of() + static_cast<long long>(it.first) * p.g;
+    const long long end = seq_row_of() + static_cast<long long>(it.qlen) * p.g;
+    uint32_t most = 0;
+    // four at a time, from the boundary before the first on (the workspace goes on behind the last)
+#pragma unroll 4
+    for (long long r = (begin & ~3ll) + 4 * (group * 32 + lane); r < end; r += 4 * 9 * 32) {
+      const uint4 w = *reinterpret_cast<const uint4*>(p.sizes + r);
+      if (r >= begin) most = max(most, w.x & 0xffffu);
+      if (r + 1 >= begin && r + 1 < end) most = max(most, w.y & 0xffffu);
+      if (r + 2 >= begin && r + 2 < end) most = max(most, w.z & 0xffffu);
+      if (r + 3 >= begin && r + 3 < end) most = max(most, w.w & 0xffffu);
+    }
+    const uint32_t of_v = size_of_v();
+    most = __reduce_max_sync(0xffffffffu, most);
+    volatile uint32_t* part = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_SIZE);
+    if (lane == 0) part[group] = most;
+    ptx::named_bar_sync(1, 9 * 32);
+#pragma unroll
+    for (int i = 0; i < 9; ++i) most = max(most, part[i]);
+    set_scale(most, of_v);
+  };
 
   if (warp >= 8) {
     ptx::reg_give<C::REGS_REST>();
@@ -566,8 +662,10 @@ __global__ void __launch_bounds__(384, 1)
       }
     } else if (warp == C::WARP_ROWS && key) {
       // ======================= statistics of the streamed rows ===============
-      const float2* base = p.stats + (static_cast<long long>(it.hk) * p.Tq + it.q0) * p.g;
       bool ok = true;
+      int of_lse[4];  // this lane's rows of a tile in lse
+#pragma unroll
+      for (int u = 0; u < 4; ++u) of_lse[u] = (lane + 32 * u) / p.g * p.Hq + it.hk * p.g + (lane + 32 * u) % p.g;
       for (int i = 0; i < n && ok; ++i) {
         const int slot = i % C::NST;
         const int tok = it.first + i * p.rt;
@@ -576,14 +674,20 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int r = lane + 32 * u;
-          v[u] = r < valid ? base[static_cast<long long>(tok) * p.g + r] : make_float2(-INFINITY, 0.0f);
+          v[u] = make_float2(-INFINITY, 0.0f);
+          if (r >= valid) continue;
+          const long long place = seq_row_of() + static_cast<long long>(tok) * p.g + r;
+          if constexpr (SCALED) v[u] = make_float2(p.lse[static_cast<long long>(it.q0 + tok) * p.Hq + of_lse[u]], p.dsum[place]);
+          else v[u] = p.stats[place];
         }
+        if (i == 0) key_scale();
         if (i >= C::NST) ok = warp_wait(bar(C::B_STE + slot), (i / C::NST - 1) & 1);
         if (!ok) break;
         float* st = reinterpret_cast<float*>(smem + C::OFF_ST + slot * 1024);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          st[lane + 32 * u] = v[u].x;
+          st[lane + 32 * u] =
+              SCALED && v[u].x != -INFINITY ? fmaf(v[u].x, -1.4426950408889634f, SHIFT) : v[u].x;
           st[128 + lane + 32 * u] = -v[u].y * c;
         }
         __syncwarp();
@@ -663,6 +767,7 @@ __global__ void __launch_bounds__(384, 1)
     auto compute = [&](auto kind) {
       constexpr bool key = decltype(kind)::value;
       // ======================= P and dS ========================================
+      if (key) key_scale();
       const int wg = warp >> 2;
       const int row = (warp & 3) * 32 + lane;  // TMEM lane
       const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -676,10 +781,19 @@ __global__ void __launch_bounds__(384, 1)
       float nl2 = -INFINITY, dcol = 0.0f;
       int limit = 0, least = 0;
       if (!key) {
+        const uint32_t of_v = SCALED && n > 0 ? size_of_v() : 0u;
         if (exists) {
-          const float2 v = p.stats[(static_cast<long long>(it.hk) * p.Tq + it.q0 + it.at) * p.g + row];
-          nl2 = v.x;
-          dcol = -v.y * c;
+          const long long place = seq_row_of() + static_cast<long long>(it.at) * p.g + row;
+          if constexpr (SCALED) {
+            const float lse = p.lse[static_cast<long long>(it.q0 + tok) * p.Hq + it.hk * p.g + row % p.g];
+            if (n > 0) set_scale(p.sizes[place] & 0xffffu, of_v);
+            nl2 = lse == -INFINITY ? -INFINITY : fmaf(lse, -1.4426950408889634f, SHIFT);
+            dcol = -p.dsum[place] * c;
+          } else {
+            const float2 v = p.stats[place];
+            nl2 = v.x;
+            dcol = -v.y * c;
+          }
         }
         limit = p.causal ? min(it.off + tok + 1, it.kvlen) : it.kvlen;
         least = p.causal ? min(it.off + it.at + 1, it.kvlen) : it.kvlen;
@@ -831,12 +945,12 @@ __global__ void __launch_bounds__(384, 1)
         const int chunks = key ? D / 32 : D / 64;
         const int c0 = key ? 0 : wg * (D / 64);
         const uint32_t acc = tmem + lane_base + (key ? (wg ? C::K_DK : C::K_DV) : C::R_DQ);
-        const float f = key && wg == 0 ? p.p_unscale : p.scale * ds_unscale;
+        const float f = (key && wg == 0 ? 1.0f : p.scale / c) * exp2f(-SHIFT);
         T* out;
         if (key) out = static_cast<T*>(wg ? p.dk : p.dv) +
-                       (static_cast<long long>(it.k0 + it.at + row) * p.Hkv + it.hk) * D;
+                       (static_cast<long long>(itemw[4] + it.at + row) * p.Hkv + itemw[1]) * D;
         else out = static_cast<T*>(p.dq) +
-                   (static_cast<long long>(it.q0 + tok) * p.Hq + it.hk * p.g + row % p.g) * D;
+                   (static_cast<long long>(itemw[2] + tok) * p.Hq + itemw[1] * p.g + row % p.g) * D;
 #pragma unroll 1
         for (int k = c0; k < c0 + chunks; ++k) {
           uint32_t r[32];

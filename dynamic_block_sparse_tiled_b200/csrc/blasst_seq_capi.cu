@@ -176,10 +176,10 @@ int check_heads(int n_seq, int Tq, int Hq, int Hkv, int d, int dtype) {
   return BLASST_OK;
 }
 
-constexpr size_t kNormBytes = 16;  // per KV head, two used words
-
+// Two words per query row, and 16 bytes per KV head that keep a call without
+// query rows from asking for none.
 size_t bwd_workspace(int Tq, int Hq, int Hkv) {
-  return static_cast<size_t>(Hkv) * kNormBytes + static_cast<size_t>(Tq) * Hq * sizeof(float2);
+  return static_cast<size_t>(Hkv) * 16 + static_cast<size_t>(Tq) * Hq * sizeof(float2);
 }
 
 template <int D, typename T>
@@ -194,11 +194,8 @@ int launch_seq_bwd(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensor
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return cuda_status(e);
   if (r.Tq > 0) {
-    if (r.norms) {
-      e = cudaMemsetAsync(r.norms, 0, static_cast<size_t>(r.Hkv) * 8, stream);
-      if (e != cudaSuccess) return cuda_status(e);
-    }
-    const int v_blocks = r.norms ? (r.Tk + blasst::kBwdRowsPerBlock - 1) / blasst::kBwdRowsPerBlock : 0;
+    // places for parts of v (seq_place)
+    const int v_blocks = blasst::SeqBwdType<T>::kScaled && r.Tk > 0 ? r.Tk / blasst::kBwdRowsPerBlock + r.n_seq : 0;
     blasst::blasst_seq_bwd_rows_kernel<D, T>
         <<<dim3(static_cast<unsigned>(r.row_blocks + v_blocks), r.Hkv), 256, 0, stream>>>(r);
     const int rc = cuda_status(cudaGetLastError());
@@ -497,13 +494,17 @@ int blasst_packed_bwd(const blasst_packed_bwd_args* a) {
   p.err = error_word();
   if (!p.err) return BLASST_ECUDA;
   const bool f16 = a->dtype == BLASST_FP16;
-  uint32_t* norms = static_cast<uint32_t*>(a->workspace);
-  float2* stats = reinterpret_cast<float2*>(static_cast<char*>(a->workspace) + a->Hkv * kNormBytes);
+  // bf16: pairs; fp16: the sizes of all rows, then D
+  float2* stats = static_cast<float2*>(a->workspace);
+  uint32_t* sizes = static_cast<uint32_t*>(a->workspace);
+  float* dsum = reinterpret_cast<float*>(sizes + static_cast<size_t>(a->Tq) * a->Hq);
   p.dq = a->dq;
   p.dk = a->dk;
   p.dv = a->dv;
   p.stats = stats;
-  p.norms = f16 ? norms : nullptr;
+  p.dsum = dsum;
+  p.sizes = sizes;
+  p.lse = a->lse;
   p.k = a->k;
   p.k_st = a->k_st;
   p.k_sh = a->k_sh;
@@ -518,8 +519,6 @@ int blasst_packed_bwd(const blasst_packed_bwd_args* a) {
   const double sc = a->scale > 0.0f ? static_cast<double>(a->scale) : 1.0 / std::sqrt(static_cast<double>(a->d));
   p.scale = static_cast<float>(sc);
   p.scale_log2 = static_cast<float>(sc * 1.4426950408889634);
-  const float shift = f16 ? blasst::seq_bwd_p_shift<__half>() : blasst::seq_bwd_p_shift<__nv_bfloat16>();
-  p.p_unscale = std::exp2(-shift);
   p.timeout_ns = kTimeoutNs;
   blasst::SeqBwdRowsParams r{};
   r.o = a->o;
@@ -527,7 +526,8 @@ int blasst_packed_bwd(const blasst_packed_bwd_args* a) {
   r.v = a->v;
   r.lse = a->lse;
   r.stats = stats;
-  r.norms = f16 ? norms : nullptr;
+  r.dsum = dsum;
+  r.sizes = sizes;
   r.cu_q = a->cu_q;
   r.cu_k = a->cu_k;
   r.o_st = a->o_st;
@@ -544,7 +544,6 @@ int blasst_packed_bwd(const blasst_packed_bwd_args* a) {
   r.g = p.g;
   r.row_blocks = static_cast<int>((static_cast<long long>(a->Tq) * p.g + blasst::kBwdRowsPerBlock - 1) /
                                   blasst::kBwdRowsPerBlock);
-  r.shift = shift;
   // a map needs an address also where no tile is ever loaded
   const void* q = a->Tq > 0 ? a->q : a->k;
   const void* dout = a->Tq > 0 ? a->dout : a->k;

@@ -465,7 +465,8 @@ BLASST_API int blasst_packed_fwd(const blasst_packed_args* args);
  * pairs, D = rowsum(dout * o) and dS = P * (dout.v - D),
  *     dq = scale dS K,  dk = scale dS^T Q,  dv = P^T dout,
  * dk and dv summed over the query heads of a KV head. The same inputs give the
- * same bits: every output row is summed by one block in one order.
+ * same bits: every output row is summed by one block in one order, and a
+ * sequence's gradients do not depend on the other sequences.
  *   q, k, v     as in the forward; o, dout [Tq, Hq, d] by strides; lse [Tq, Hq]
  *               contiguous, the forward's for these inputs.
  *   dq [Tq, Hq, d], dk, dv [Tk, Hkv, d]: contiguous, in the inputs' type. Rows
@@ -497,8 +498,8 @@ typedef struct blasst_packed_bwd_args {
 } blasst_packed_bwd_args;
 BLASST_API int blasst_packed_bwd(const blasst_packed_bwd_args* args);
 
-/* Workspace bytes of blasst_packed_bwd: two fp32 statistics per query row and
- * 16 bytes per KV head (0 for arguments out of range). Host only. */
+/* Workspace bytes of blasst_packed_bwd: two words per query row and 16 bytes
+ * per KV head (0 for arguments out of range). Host only. */
 BLASST_API size_t blasst_packed_bwd_workspace_bytes(int Tq, int Hq, int Hkv);
 
 /* Attention of new tokens (a chunk, or one per sequence) over the paged cache,
