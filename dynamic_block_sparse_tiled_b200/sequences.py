@@ -66,10 +66,11 @@ def rope_frequencies(rot, *, base=10000.0, scaling="none", factor=1.0, original_
       none    f_i;
       linear  f_i / factor (positions interpolated);
       ntk     base * factor^(rot / (rot - 2)) in the place of base;
-      blend   pairs that turn at least ``high`` (32) times over ``original_len``
-              positions are kept, those of at most ``low`` (1) turns divided by
-              factor, a straight line over the pair's index between; factor for
-              the dims 0.1 ln(factor) + 1;
+      blend   (YaRN) pairs that turn at least ``high`` (32) times over
+              ``original_len`` positions are kept, those of at most ``low`` (1)
+              turns divided by factor, a straight line over the pair's index
+              (from 0 on at the earliest) between; factor for the dims
+              0.1 ln(factor) + 1;
       bands   as blend over the number of turns, from ``low`` (1) to ``high`` (4),
               and a factor of 1 for the dims.
     """
@@ -95,9 +96,10 @@ def rope_frequencies(rot, *, base=10000.0, scaling="none", factor=1.0, original_
         if not 0.0 < lo < hi:
             raise ValueError("low must be over 0 and under high")
         if scaling == "blend":
-            # pair index at which a pair turns n times over original_len positions
+            # pair index at which a pair turns n times over original_len positions; where the
+            # last pair turns more than lo times, the line ends behind the table
             at = lambda n: rot * math.log(original_len / (n * 2.0 * math.pi)) / (2.0 * math.log(base))  # noqa: E731
-            first, last = max(math.floor(at(hi)), 0), min(math.ceil(at(lo)), rot // 2 - 1)
+            first, last = max(math.floor(at(hi)), 0), math.ceil(at(lo))
             keep = 1.0 - ((i - first) / max(last - first, 1e-3)).clamp(0.0, 1.0)
             if factor > 1.0:
                 mscale = 0.1 * math.log(factor) + 1.0
