@@ -83,39 +83,47 @@ int cuda_status(cudaError_t e) {
   return BLASST_ECUDA;
 }
 
+// Encodes a tiled tensor map, zero fill outside. The driver's call needs a current
+// context, and a host thread that has made no CUDA call before (a worker of
+// autograd's, or of a server) has none: the current device's is then bound.
+bool encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, int rank, void* base, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  auto enc = encoder();
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  auto run = [&]() -> CUresult {
+    return enc(map, dt, rank, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = enc ? run() : CUDA_ERROR_NOT_FOUND;
+  int dev = 0;
+  if ((r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) && cudaGetDevice(&dev) == cudaSuccess &&
+      cudaSetDevice(dev) == cudaSuccess)
+    r = run();
+  if (r != CUDA_SUCCESS) g_last_cuda_error = "a tensor map could not be encoded";
+  return r == CUDA_SUCCESS;
+}
+
 // 3-D map over a dense [heads, L, d] tensor: dims (d, L, heads), box
 // (64 columns, rows, 1), 128-byte swizzle, zero fill outside the tensor.
 bool make_map(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes,
               int d, int L, int heads, int box_rows) {
-  auto enc = encoder();
-  if (!enc) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(L),
                         static_cast<cuuint64_t>(heads)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * elem_bytes,
                            static_cast<cuuint64_t>(d) * elem_bytes * L};
   cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem_bytes),
                        static_cast<cuuint32_t>(box_rows), 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  return encode_tiled(map, dt, 3, const_cast<void*>(base), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // 3-D map over a dense fp32 [heads, L, d] tensor without swizzle, box
 // (32 columns, rows, 1): the target of TMA reduce-adds.
 bool make_map_f32_plain(CUtensorMap* map, void* base, int d, int L, int heads, int box_rows) {
-  auto enc = encoder();
-  if (!enc) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(L),
                         static_cast<cuuint64_t>(heads)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 4, static_cast<cuuint64_t>(d) * 4 * L};
   cuuint32_t box[3] = {32, static_cast<cuuint32_t>(box_rows), 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 template <typename K>
@@ -244,7 +252,10 @@ float log2_lambda_of(float lambda) {
 namespace blasst {
 namespace capi {
 int* error_word() { return ::error_word(); }
-PFN_cuTensorMapEncodeTiled_v12000 encoder() { return ::encoder(); }
+bool encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, int rank, void* base, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  return ::encode_tiled(map, dt, rank, base, dims, strides, box, swizzle);
+}
 int cuda_status(cudaError_t e) { return ::cuda_status(e); }
 }  // namespace capi
 }  // namespace blasst

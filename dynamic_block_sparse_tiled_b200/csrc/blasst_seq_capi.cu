@@ -17,7 +17,7 @@
 namespace {
 
 using blasst::capi::cuda_status;
-using blasst::capi::encoder;
+using blasst::capi::encode_tiled;
 using blasst::capi::error_word;
 using blasst::capi::kTimeoutNs;
 
@@ -41,20 +41,15 @@ int sm_count() {
 // outside. Strides in elements of 2 bytes.
 bool make_map4(CUtensorMap* map, const void* base, int dtype, const long long (&dim)[4],
                const long long (&stride)[3], int box1, int box2) {
-  auto enc = encoder();
-  if (!enc) return false;
   cuuint64_t dims[4], strides[3];
   for (int i = 0; i < 4; ++i) dims[i] = static_cast<cuuint64_t>(dim[i] > 0 ? dim[i] : 1);
   // the stride of a dimension of one entry is never used, but has to be valid
   for (int i = 0; i < 3; ++i)
     strides[i] = dims[i + 1] == 1 ? 16 : static_cast<cuuint64_t>(stride[i]) * 2;
   cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2), 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
   const auto dt = dtype == BLASST_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  return enc(map, dt, 4, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(map, dt, 4, const_cast<void*>(base), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // A stride a tensor map can hold: positive, a multiple of 16 bytes, < 2^40.

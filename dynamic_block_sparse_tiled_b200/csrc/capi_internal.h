@@ -15,8 +15,10 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per bounded wait
 // The address of the two device error words (waits that gave up, index errors)
 // on the current device, or null.
 int* error_word();
-// cuTensorMapEncodeTiled, or null.
-PFN_cuTensorMapEncodeTiled_v12000 encoder();
+// A tiled tensor map with zero fill outside; false if it cannot be had. Works on
+// host threads without a current context.
+bool encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, int rank, void* base, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle);
 // BLASST_OK or BLASST_ECUDA, with the error's text kept for
 // blasst_last_cuda_error().
 int cuda_status(cudaError_t e);
