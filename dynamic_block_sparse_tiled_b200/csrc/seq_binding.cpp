@@ -6,6 +6,7 @@
 // in Python through ctypes took 15 to 35 us a call, here it takes about 2.
 // sequences.py holds the documented functions that call in here.
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -43,11 +44,21 @@ int dtype_of(const Tensor& t) {
   }
 }
 
+// The calls record nothing for autograd: a tensor whose gradient is asked for
+// would lose it without a word. (Within an autograd function nothing is recorded.)
+void no_gradient(const Tensor& t) {
+  if (at::GradMode::is_enabled() && t.requires_grad())
+    refuse(
+        "a tensor requires a gradient, which this call does not record: call it under torch.no_grad() or in a "
+        "torch.autograd.Function, with rotary_backward or attention_packed_backward for the gradients");
+}
+
 // The device of a call, its first tensor's (the rest is checked against it),
 // and its stream, current while the call allocates.
 class Call {
  public:
   Call(const Tensor& first, const Stream& given) {
+    no_gradient(first);
     if (!first.is_cuda()) refuse("tensors passed to the CUDA library must live on a CUDA device");
     device_ = first.get_device();
     guard_.set_index(device_);
@@ -71,6 +82,7 @@ class Call {
   // (on a stream of the caller's choice, a tensor that is freed behind the call
   // stays until the kernel has read it)
   void here(const Tensor& t) const {
+    no_gradient(t);
     if (!t.is_cuda() || t.get_device() != device_) refuse("tensors must live on one CUDA device");
     if (given_) t.record_stream(*given_);
   }

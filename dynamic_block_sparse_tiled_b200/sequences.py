@@ -9,6 +9,11 @@ and the checks made on the device. Packed tokens are ``[T, heads, d]``; any
 token and head strides are taken as long as ``d`` is contiguous. Lengths and
 page tables stay on the device: a call neither synchronises nor reads them, and
 a captured call may be replayed after they have changed.
+
+Autograd records none of the calls. Tensors that require a gradient are refused
+(ValueError) unless gradients are off, as they are under ``torch.no_grad()`` and
+within a ``torch.autograd.Function``, whose backward then calls
+``rotary_backward`` and ``attention_packed_backward``.
 """
 from __future__ import annotations
 
