@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -25,15 +26,16 @@ constexpr int kMaxDevices = 64;
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// SMs of the current device (a host-side query, kept per device).
+// SMs of the current device (a host-side query, kept per device; host threads may
+// find it at the same time).
 int sm_count() {
-  static int known[kMaxDevices] = {0};
+  static std::atomic<int> known[kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
-  if (dev < kMaxDevices && known[dev] > 0) return known[dev];
-  int n = 0;
+  int n = dev < kMaxDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  if (dev < kMaxDevices) known[dev] = n;
+  if (dev < kMaxDevices) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -62,14 +64,16 @@ size_t seq_workspace(int sms, int d) {
 // The register split of a kernel waits for registers the launch must have:
 // refused (not run) if a build gave the kernel fewer.
 template <typename K>
-int check_regs(K kernel, int regs, int& known) {
-  if (known == 0) {
+int check_regs(K kernel, int regs, std::atomic<int>& known) {
+  int have = known.load(std::memory_order_relaxed);
+  if (have == 0) {
     cudaFuncAttributes fa;
     const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess) return cuda_status(e);
-    known = fa.numRegs;
+    have = fa.numRegs;
+    known.store(have, std::memory_order_relaxed);
   }
-  return known >= regs ? BLASST_OK : BLASST_EUNSUPPORTED;
+  return have >= regs ? BLASST_OK : BLASST_EUNSUPPORTED;
 }
 
 // A launch that may begin while the kernel before it runs; the kernel waits for
@@ -94,7 +98,7 @@ int launch_seq(const CUtensorMap& mq, const CUtensorMap& mq_few, const CUtensorM
                const CUtensorMap& mv, const blasst::SeqAttnParams& p, int sms, cudaStream_t stream) {
   using C = blasst::SeqAttnCfg<D, FEW>;
   auto kernel = blasst::blasst_seq_attn_kernel<D, T, FEW>;
-  static int regs = 0;  // of this instantiation
+  static std::atomic<int> regs{0};  // of this instantiation
   if (const int rc = check_regs(kernel, C::REGS, regs)) return rc;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
@@ -183,7 +187,7 @@ int launch_seq_bwd(const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensor
                    const blasst::SeqBwdRowsParams& r, cudaStream_t stream) {
   using C = blasst::SeqBwdCfg<D>;
   auto kernel = blasst::blasst_seq_bwd_kernel<D, T>;
-  static int regs = 0;  // of this instantiation
+  static std::atomic<int> regs{0};  // of this instantiation
   if (const int rc = check_regs(kernel, C::REGS, regs)) return rc;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);

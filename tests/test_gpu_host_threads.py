@@ -84,3 +84,34 @@ def test_first_call_of_a_thread(bl, name):
             assert float((a - b).norm()) <= 16 * 300 * 2.0 ** -24 * float(b.norm())
         else:
             assert torch.equal(a, b), i
+
+
+def test_threads_at_once(bl):
+    """Several threads, each with a stream of its own, beginning together."""
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(71)
+    lens = [100, 333, 7]
+    q, k, v, dout = (torch.randn(440, h, 64, generator=g, device="cuda").half() for h in (4, 2, 2, 4))
+    cu = R.cu(lens)
+    o, lse = bl.attention_packed(q, k, v, cu)
+    want = (o, lse, *bl.attention_packed_backward(q, k, v, o, lse, dout, cu))
+    torch.cuda.synchronize()
+    start, got = threading.Barrier(6, timeout=60), [None] * 6
+
+    def run(i):
+        start.wait()
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(5):
+                a, b = bl.attention_packed(q, k, v, cu)
+                got[i] = (a, b, *bl.attention_packed_backward(q, k, v, a, b, dout, cu))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    torch.cuda.synchronize()
+    for result in got:
+        assert result is not None and all(torch.equal(a, b) for a, b in zip(result, want))
+    assert bl.blasst_check() == 0
