@@ -318,7 +318,8 @@ int blasst_rotary(const blasst_rotary_args* a) {
 }
 
 int blasst_append(const blasst_append_args* a) {
-  if (!a || !a->k || !a->v || !a->k_pages || !a->v_pages || !a->page_table || !a->kv_lens ||
+  // (without sequences there are no lengths and no table)
+  if (!a || !a->k || !a->v || !a->k_pages || !a->v_pages || (a->n_seq > 0 && (!a->page_table || !a->kv_lens)) ||
       !a->cu_q || (a->q == nullptr) != (a->q_out == nullptr))
     return BLASST_EINVAL;
   if (a->dtype != BLASST_BF16 && a->dtype != BLASST_FP16 && a->dtype != BLASST_FP32)
@@ -565,8 +566,9 @@ int blasst_packed_bwd(const blasst_packed_bwd_args* a) {
 }
 
 int blasst_paged_fwd(const blasst_paged_args* a) {
-  if (!a || !a->q || !a->k_pages || !a->v_pages || !a->o || !a->lse || !a->page_table ||
-      !a->kv_lens || !a->cu_q)
+  // (without sequences there are no lengths and no table)
+  if (!a || !a->q || !a->k_pages || !a->v_pages || !a->o || !a->lse || !a->cu_q ||
+      (a->n_seq > 0 && (!a->page_table || !a->kv_lens)))
     return BLASST_EINVAL;
   for (const void* ptr : {a->q, a->k_pages, a->v_pages, static_cast<const void*>(a->o),
                           static_cast<const void*>(a->lse)})
