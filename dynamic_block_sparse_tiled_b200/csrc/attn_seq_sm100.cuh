@@ -50,12 +50,16 @@
 // reference lies 2^7 under the row's maximum for its range, SeqType), and
 // o once at the end.
 //
-// What bounds it. Long prompts: the tensor core with its issue, about 95 cycles
-// per 128 x 128 x 16 product beside the softmax's TMEM traffic (64 ideal; 32768
-// prompt tokens of 32 / 8 heads of 128, bf16: 2.74 ms, 1.14 PFLOP/s). Single
-// tokens: memory (16 x 65536 cached tokens of 8 KV heads of 128: 645-680 us,
-// 0.97 of a copy's rate). Short calls: latency (511 tokens in 5 prompts: 12 us
-// on the GPU, 2 of set-up, 1.5 to find the item, 1.5 for the first loads).
+// What bounds it ("cool": single passes at 1.7 GHz or more; passes in a row run at
+// the card's power cap). Long prompts: the tensor core with its issue, about 95
+// cycles per 128 x 128 x 16 product beside the softmax's TMEM traffic (64 ideal;
+// 32768 prompt tokens of 32 / 8 heads of 128, bf16: 2.76 ms cool, 1.13 PFLOP/s;
+// 3.20 ms in a row, 0.97). Heads of 64: the exponentials with the same (14250
+// tokens in two prompts of 64 / 8 heads, causal: 1.53 ms, where 16 exponentials a
+// cycle take 0.75 and the products 0.52). Single tokens: memory (16 x 65536 cached
+// tokens of 8 KV heads of 128: 650-740 us by how the pages lie, 0.90-0.97 of a
+// copy's rate). Short calls: latency (511 tokens in 5 prompts: 13 us on the GPU, 2
+// of set-up, 1.5 to find the item, 1.5 for the first loads).
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>

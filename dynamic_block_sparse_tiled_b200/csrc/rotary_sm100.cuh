@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(256, 3) blasst_rotary_kernel(const RotaryParam
 // its page (sequence, length, table entry, angles) is a chain of dependent reads
 // of about 3 us, so a block takes as many tokens as there are to keep it busy:
 // 2560 tokens of 48 heads of 128, fp16, on warm inputs: 12.5 us (5.0 TB/s, 78 % of
-// a copy's rate) with four, 14.3 us with one; on changing ones 18.5 us with four,
-// 18.3 us with eight.
+// a copy's rate) with four, 14.3 us with one; on changing ones 18.4 us with eight
+// (3.4 TB/s) and 18.5 us with four, which is no difference.
 constexpr int kAppendTokens = 8;  // most tokens of a block, one warp each to find its place
 
 template <typename T, int VEC, bool IL>

@@ -406,7 +406,7 @@ BLASST_API int blasst_rotary(const blasst_rotary_args* args);
  *   freq       as in blasst_rotary; NULL (with rot = 0): nothing is turned.
  * Pages not named by the new tokens are not touched. A token whose place is
  * out of range is not written (BLASST_EINDEX). Two tokens with the same place
- * (a table that names a page twice) leave one of them there. */
+ * (a table that names a page twice) leave parts of either there. */
 typedef struct blasst_append_args {
   const void* q;
   void* q_out;
@@ -435,6 +435,9 @@ BLASST_API int blasst_append(const blasst_append_args* args);
  * of the sequence (causal = 0). Rows without keys get o = 0, lse = -inf.
  * The weights are rounded to the inputs' type before they meet the values
  * (fp16: with an absolute error of at most 2^-32 of the row's largest weight).
+ * A value that is infinite or NaN also reaches rows of its sequence that the
+ * mask keeps from it, where they share a block of 128 keys (0 x NaN); what
+ * lies outside the sequences may hold anything.
  *   q [Tq, Hq, d], k, v [Tk, Hkv, d] by strides; o [Tq, Hq, d] and lse
  *   [Tq, Hq] (fp32, natural log) contiguous.
  *   cu_q, cu_k  device int32 [n_seq + 1].
